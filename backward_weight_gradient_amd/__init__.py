@@ -61,6 +61,10 @@ class forge_state(ctypes.Structure):
     _fields_ = [("q", forge_mat), ("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
 
 
+class forge_act8(ctypes.Structure):
+    _fields_ = [("q", forge_mat), ("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
+
+
 class forge_hyper(ctypes.Structure):
     _fields_ = [("opt", ctypes.c_int32), ("round", ctypes.c_int32), ("lr", ctypes.c_double),
                 ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
@@ -130,6 +134,35 @@ def _load() -> ctypes.CDLL:
                                               P(forge_state), P(forge_hyper), ctypes.c_int64, ctypes.c_uint64,
                                               P(forge_mat), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
     lib.forge_backward_step_split.restype = st
+    mats = P(forge_mat)
+    vp, i32, i64, f64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_double
+    lib.forge_act_quantize.argtypes = [mats, P(forge_act8), vp]
+    lib.forge_act_quantize.restype = st
+    lib.forge_act_dequantize.argtypes = [P(forge_act8), mats, vp]
+    lib.forge_act_dequantize.restype = st
+    lib.forge_wgrad_step_act8.argtypes = [P(forge_act8), mats, mats, P(forge_state), P(forge_state), P(forge_hyper),
+                                          i64, ctypes.c_uint64, vp]
+    lib.forge_wgrad_step_act8.restype = st
+    lib.forge_wgrad_check_act8.argtypes = [P(forge_act8), mats, mats, P(forge_state), P(forge_state),
+                                           P(forge_hyper), i64]
+    lib.forge_wgrad_check_act8.restype = st
+    lib.forge_wgrad_accumulate_act8.argtypes = [P(forge_act8), mats, mats, i32, vp]
+    lib.forge_wgrad_accumulate_act8.restype = st
+    lib.forge_rmsnorm.argtypes = [mats, mats, mats, f64, mats, mats, P(forge_act8), vp, vp]
+    lib.forge_rmsnorm.restype = st
+    lib.forge_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    lib.forge_rmsnorm_workspace_bytes.restype = i64
+    lib.forge_rmsnorm_backward.argtypes = [mats, mats, mats, vp, mats, mats, vp, i32, vp, i64, vp]
+    lib.forge_rmsnorm_backward.restype = st
+    lib.forge_embed.argtypes = [vp, i32, i64, mats, f64, mats, vp]
+    lib.forge_embed.restype = st
+    lib.forge_embed_workspace_bytes.argtypes = [i64, i64]
+    lib.forge_embed_workspace_bytes.restype = i64
+    lib.forge_embed_accumulate.argtypes = [vp, i32, i64, mats, f64, mats, i32, vp, i64, vp]
+    lib.forge_embed_accumulate.restype = st
+    lib.forge_embed_step.argtypes = [vp, i32, i64, mats, f64, mats, P(forge_state), P(forge_state), P(forge_hyper),
+                                     i64, ctypes.c_uint64, vp, i64, vp]
+    lib.forge_embed_step.restype = st
     lib.forge_debug_e4m3.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]
     lib.forge_debug_e4m3.restype = st
     lib.forge_debug_e4m3_sr.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_uint64,
@@ -162,13 +195,15 @@ lib = _load()
 # ---------------------------------------------------------------------------
 # Struct builders
 # ---------------------------------------------------------------------------
+_CODES = {torch.float32: FORGE_F32, torch.bfloat16: FORGE_BF16, torch.int8: FORGE_S8, torch.uint8: FORGE_U8,
+          torch.float8_e4m3fn: FORGE_E4M3}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: FORGE_F32, torch.bfloat16: FORGE_BF16, torch.int8: FORGE_S8, torch.uint8: FORGE_U8,
-             torch.float8_e4m3fn: FORGE_E4M3}
-    if t.dtype not in codes:
+    code = _CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported tensor dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def mat_raw(ptr: int, dtype: int, rows: int, cols: int, ld: Optional[int] = None) -> forge_mat:
@@ -202,6 +237,20 @@ def state(t, scale=None, block: int = 0) -> forge_state:
     if scale.numel() != t.shape[0] * (t.shape[1] // block):
         raise ValueError(f"state: {scale.numel()} scales given, {t.shape[0] * (t.shape[1] // block)} needed")
     return forge_state(mat(t), scale.data_ptr() or None, block)
+
+
+def act8(codes, scale, block: int) -> forge_act8:
+    """A forge_act8: int8 or float8_e4m3fn codes [rows, cols] and their uint8 scale
+    bytes, a contiguous [rows, ceil(cols / block)] tensor on the codes' device,
+    block in {32, 64, 128}."""
+    if block not in (32, 64, 128):
+        raise ValueError(f"act8: block must be 32, 64 or 128, got {block}")
+    q = mat(codes)
+    if scale.dtype != torch.uint8 or not scale.is_contiguous() or scale.device != codes.device:
+        raise ValueError("act8: the scale tensor must be contiguous uint8 on the codes' device")
+    if scale.numel() != q.rows * -(-q.cols // block):
+        raise ValueError(f"act8: {scale.numel()} scales given, {q.rows * -(-q.cols // block)} needed")
+    return forge_act8(q, scale.data_ptr() or None, block)
 
 
 def hyper(opt: str = "adamw", lr: float = 1e-3, beta1: float = 0.9, beta2: Optional[float] = None,
@@ -429,6 +478,166 @@ def forge_wgrad_unfused(X, dY, W, m, v, h: forge_hyper, step: int, seed: int, dW
     if check and rc != FORGE_OK:
         raise ForgeError(rc, "forge_wgrad_unfused")
     return rc
+
+
+class _Launch:
+    """The stream of a call and the device it belongs to: that of its tensors, which
+    need not be the current one.  Tensor arguments must all be on one device;
+    structs made from raw pointers say nothing about theirs."""
+
+    __slots__ = ("device",)
+
+    def __init__(self, *args):
+        self.device = None
+        for a in args:
+            if isinstance(a, torch.Tensor):
+                if self.device is None:
+                    self.device = a.device
+                elif a.device != self.device:
+                    raise ValueError(f"tensors on {self.device} and {a.device} in one call")
+
+    def __call__(self, name, stream, check, fn, *args):
+        d = self.device
+        if d is None or d.type != "cuda" or d.index == torch.cuda.current_device():
+            rc = fn(*args, _stream(stream))
+        else:
+            with torch.cuda.device(d):
+                rc = fn(*args, _stream(stream))
+        if check and rc != FORGE_OK:
+            raise ForgeError(rc, name)
+        return rc
+
+
+def _as_mat(t):
+    return t if t is None or isinstance(t, forge_mat) else mat(t)
+
+
+def _row_mat(t):
+    """A 1-D tensor as a [1, n] matrix (a forge_mat or a 2-D tensor as it is)."""
+    if t is None or isinstance(t, forge_mat):
+        return t
+    if t.dim() == 1:
+        if t.numel() > 1 and t.stride(0) != 1:
+            raise ValueError("expected a contiguous vector")
+        return forge_mat(t.data_ptr() or None, _dtype_code(t), 1, t.numel(), max(1, t.numel()))
+    return mat(t)
+
+
+def _floats(t, n: int, what: str):
+    """The address of a contiguous float32 tensor of n elements (or None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{what} must be contiguous float32 with {n} elements")
+    return t.data_ptr() or None
+
+
+def _workspace(t):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.data_ptr() or None, t.numel() * t.element_size()
+
+
+def _ids(ids):
+    """(address, bytes per id, tokens) of a contiguous int32 / int64 vector of token ids."""
+    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 or int64 tensor")
+    return ids.data_ptr() or None, ids.element_size(), ids.numel()
+
+
+def forge_act_quantize(X, Q: forge_act8, stream=None, check: bool = True) -> int:
+    """Q (codes and power-of-two block scales) = X in 8 bits; Q from act8()."""
+    return _Launch(X)("forge_act_quantize", stream, check, lib.forge_act_quantize, _ref(_as_mat(X)), _ref(Q))
+
+
+def forge_act_dequantize(Q: forge_act8, X, stream=None, check: bool = True) -> int:
+    """X (bf16 or float32) = the values Q holds, exactly."""
+    return _Launch(X)("forge_act_dequantize", stream, check, lib.forge_act_dequantize, _ref(Q), _ref(_as_mat(X)))
+
+
+def forge_wgrad_step_act8(X: forge_act8, dY, W, m, v, h: forge_hyper, step: int, seed: int, stream=None,
+                          check: bool = True) -> int:
+    """forge_wgrad_step with X from its 8-bit copy (dY bf16)."""
+    return _Launch(dY, W)("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, _ref(X),
+                          _ref(_as_mat(dY)), _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed)
+
+
+def forge_wgrad_check_act8(X: forge_act8, dY: forge_mat, W: forge_mat, m, v, h: forge_hyper, step: int) -> int:
+    return lib.forge_wgrad_check_act8(_ref(X), _ref(dY), _ref(W), _ref(m), _ref(v), _ref(h), step)
+
+
+def forge_wgrad_accumulate_act8(X: forge_act8, dY, acc, first: bool, stream=None, check: bool = True) -> int:
+    """forge_wgrad_accumulate with X from its 8-bit copy (dY bf16)."""
+    return _Launch(dY, acc)("forge_wgrad_accumulate_act8", stream, check, lib.forge_wgrad_accumulate_act8, _ref(X),
+                            _ref(_as_mat(dY)), _ref(_as_mat(acc)), 1 if first else 0)
+
+
+def forge_rmsnorm(X, gamma, Y=None, eps: float = 1e-5, R=None, H=None, Q: Optional[forge_act8] = None, rstd=None,
+                  stream=None, check: bool = True) -> int:
+    """H = X + R; Y = H / sqrt(mean(H^2) + eps) * gamma, and Q its 8-bit copy.
+
+    gamma: [cols] or [1, cols]; R and H together or not at all; rstd: float32
+    [rows], kept for forge_rmsnorm_backward.  Every output but one may be None.
+    """
+    x = _as_mat(X)
+    return _Launch(X, gamma, Y, R, H, rstd)(
+        "forge_rmsnorm", stream, check, lib.forge_rmsnorm, _ref(x), _ref(_as_mat(R)), _ref(_row_mat(gamma)), eps,
+        _ref(_as_mat(H)), _ref(_as_mat(Y)), _ref(Q), _floats(rstd, x.rows, "rstd"))
+
+
+def forge_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
+    """Bytes of workspace forge_rmsnorm_backward uses for dgamma."""
+    return int(lib.forge_rmsnorm_workspace_bytes(rows, cols))
+
+
+def forge_rmsnorm_backward(dY, H, gamma, rstd, dX=None, dR=None, dgamma=None, first: bool = True, workspace=None,
+                           stream=None, check: bool = True) -> int:
+    """dX = the norm's input gradient (+ dR); dgamma = (first) or += the sum over rows
+    of dY * H * rstd (float32 [cols]).  The workspace, a device tensor of at least
+    forge_rmsnorm_workspace_bytes bytes, is needed for dgamma only."""
+    h = _as_mat(H)
+    ws, nbytes = _workspace(workspace)
+    return _Launch(dY, H, gamma, rstd, dX, dR, dgamma, workspace)(
+        "forge_rmsnorm_backward", stream, check, lib.forge_rmsnorm_backward, _ref(_as_mat(dY)), _ref(h),
+        _ref(_row_mat(gamma)), _floats(rstd, h.rows, "rstd"), _ref(_as_mat(dR)), _ref(_as_mat(dX)),
+        _floats(dgamma, h.cols, "dgamma"), 1 if first else 0, ws, nbytes)
+
+
+def forge_embed(ids, W, Y, scale: float = 1.0, stream=None, check: bool = True) -> int:
+    """Y[t] = scale * W[ids[t]]; a row of zeros where the id is outside W's rows."""
+    ptr, width, T = _ids(ids)
+    return _Launch(ids, W, Y)("forge_embed", stream, check, lib.forge_embed, ptr, width, T, _ref(_as_mat(W)), scale,
+                              _ref(_as_mat(Y)))
+
+
+def forge_embed_workspace_bytes(T: int, V: int) -> int:
+    """Bytes of workspace the embedding's gradient uses for T tokens and V rows."""
+    return int(lib.forge_embed_workspace_bytes(T, V))
+
+
+def forge_embed_accumulate(ids, dY, acc, first: bool, scale: float = 1.0, workspace=None, stream=None,
+                           check: bool = True) -> int:
+    """acc = G (first) or acc += G, the embedding's gradient G[v] = scale * sum of dY[t]
+    over the tokens with id v (acc float32; rows that do not occur are left alone by
+    the addition)."""
+    ptr, width, T = _ids(ids)
+    ws, nbytes = _workspace(workspace)
+    return _Launch(ids, dY, acc, workspace)(
+        "forge_embed_accumulate", stream, check, lib.forge_embed_accumulate, ptr, width, T, _ref(_as_mat(dY)), scale,
+        _ref(_as_mat(acc)), 1 if first else 0, ws, nbytes)
+
+
+def forge_embed_step(ids, dY, W, m, v, h: forge_hyper, step: int, seed: int, scale: float = 1.0, workspace=None,
+                     stream=None, check: bool = True) -> int:
+    """The optimizer step of forge_wgrad_step on the embedding's gradient, for every
+    row of W, in place on W / m / v."""
+    ptr, width, T = _ids(ids)
+    ws, nbytes = _workspace(workspace)
+    return _Launch(ids, dY, W, workspace)(
+        "forge_embed_step", stream, check, lib.forge_embed_step, ptr, width, T, _ref(_as_mat(dY)), scale,
+        _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed, ws, nbytes)
 
 
 def forge_debug_e4m3(inp, out, stream=None, check: bool = True) -> int:

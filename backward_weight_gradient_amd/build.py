@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libforge.so")
 # forge_device.h holds the kernels (all templates); each forge_k_*.hip
 # instantiates one optimizer family's, so the families compile in parallel.
-SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip")) + ["forge_dispatch.cpp", "forge_api.cpp"]
+SOURCES = sorted(f for f in os.listdir(CSRC) if f.endswith(".hip")) + ["forge_dispatch.cpp", "forge_api.cpp", "forge_api_act.cpp"]
 
 # -ffp-contract=off: the step's fp32 op sequence is exactly the written one
 # (explicit fmaf only).  Packed-fp32 instructions are disabled.

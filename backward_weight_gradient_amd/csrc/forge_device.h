@@ -777,10 +777,10 @@ template <> struct MainSel<FMT_BF16> { using T = MainBF16; };
 template <> struct MainSel<FMT_F32> { using T = MainF32; };
 
 // Phase 1 of Algorithm 1 for tile (row0, col0), then the fp32 tile in LDS:
-// sG[r * GP + c] = G[row0 + r][col0 + c].
-template <int IN>
-__device__ __forceinline__ void tile_gradient(const KArgs& a, char* lds, int row0, int col0) {
-  using M = typename MainSel<IN>::T;
+// sG[r * GP + c] = G[row0 + r][col0 + c].  M: the loader and MFMA loop, A: its
+// arguments.
+template <class M, class A>
+__device__ __forceinline__ void tile_gradient_by(const A& a, char* lds, int row0, int col0) {
   static_assert(2 * M::STAGE <= LDS_BYTES, "LDS budget");
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wr = wave >> 1, wc = wave & 1;
@@ -819,6 +819,10 @@ __device__ __forceinline__ void tile_gradient(const KArgs& a, char* lds, int row
         sG[r * GP + c] = acc[bi][bj][e];
       }
   __syncthreads();
+}
+template <int IN>
+__device__ __forceinline__ void tile_gradient(const KArgs& a, char* lds, int row0, int col0) {
+  tile_gradient_by<typename MainSel<IN>::T>(a, lds, row0, col0);
 }
 
 // ------------------------------------------------------------------------

@@ -1,0 +1,116 @@
+// The optimizer step on an embedding's gradient: the fused step's epilogue on
+// tiles whose gradient is gathered from the sorted tokens.
+#pragma once
+
+#include "forge_act8.h"
+
+namespace forge {
+
+// G tile (128 rows of W from row0, 128 columns from col0) into LDS:
+//   sG[r * GP + c] = scale * sum over the tokens of row row0 + r of dY[token][col0 + c].
+// 16 lanes of 8 columns per token.  A row of up to LONG_ROW tokens belongs to one
+// wave, 4 tokens at a time; a longer one to the whole workgroup, 16 at a time.
+// Sums over a slot's tokens in order, then over the slots in a fixed order.
+// red: 3 x 128 floats.
+constexpr int LONG_ROW = 32;
+
+template <int DF>
+__device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int n, int step, int64_t c, float (&s)[8]) {
+  constexpr int ds = DF == FMT_F32 ? 4 : 2;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s[k] = 0.f;
+#pragma unroll 2
+  for (int i = first; i < n; i += step) {
+    float x[8];
+    row_load8<DF>(static_cast<const char*>(e.dY) + (int64_t)e.perm[i] * e.lddy * ds, c, e.K, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] += x[k];
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    s[k] += __shfl_xor(s[k], 16);
+    s[k] += __shfl_xor(s[k], 32);
+  }
+}
+
+template <int DF>
+__device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* rng, float* red, int row0, int col0) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int cl = 8 * (lane & 15);
+  const int64_t c = (int64_t)col0 + cl;
+  if (tid < TILE) {
+    const bool in = (int64_t)row0 + tid < e.V;
+    rng[2 * tid] = in ? e.start[row0 + tid] : 0;
+    rng[2 * tid + 1] = in ? e.end[row0 + tid] : 0;
+  }
+  for (int i = tid; i < TILE * GP / 4; i += NT) reinterpret_cast<f32x4*>(sG)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = half * 64 + lane;
+    const int n = rng[2 * r + 1] - rng[2 * r];
+    // rows of this wave (r % 4 == wave) with few tokens, then the long rows with all waves
+    uint64_t mine = __ballot(n > 0 && n <= LONG_ROW && (r & 3) == wave), all = __ballot(n > LONG_ROW);
+    while (mine) {
+      const int k = half * 64 + __builtin_ctzll(mine);
+      mine &= mine - 1;
+      float s[8];
+      gather_tokens<DF>(e, rng[2 * k] + (lane >> 4), rng[2 * k + 1], 4, c, s);
+      if (lane < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sG[k * GP + cl + i] = s[i] * e.scale;
+      }
+    }
+    while (all) {   // the same rows in every wave
+      const int k = half * 64 + __builtin_ctzll(all);
+      all &= all - 1;
+      float s[8];
+      gather_tokens<DF>(e, rng[2 * k] + (tid >> 4), rng[2 * k + 1], 16, c, s);
+      if (wave > 0 && lane < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[(wave - 1) * TILE + cl + i] = s[i];
+      }
+      __syncthreads();
+      if (wave == 0 && lane < 16) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sG[k * GP + cl + i] =
+              (((s[i] + red[cl + i]) + red[TILE + cl + i]) + red[2 * TILE + cl + i]) * e.scale;
+      }
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+}
+
+template <bool FAST, int OPT, int WF, int MF, int VF>
+__global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const EmbedArgs e) {
+  __shared__ __attribute__((aligned(16))) float sG[TILE * GP];
+  __shared__ int rng[2 * TILE];
+  __shared__ float red[3 * TILE];
+  int ti, tj;
+  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
+  const int row0 = ti * TILE, col0 = tj * TILE;
+  Epilogue<Step<OPT, WF, MF, VF, FAST>, FMT_NONE, FAST, 4> epi;
+  epi.tid = threadIdx.x;
+  epi.prefetch(a, row0, col0);
+  if (e.dy_fmt == FMT_F32) embed_tile<FMT_F32>(e, sG, rng, red, row0, col0);
+  else embed_tile<FMT_BF16>(e, sG, rng, red, row0, col0);
+  epi.run_prefetched(a, sG, row0, col0);
+}
+
+template <int O, int M, int V>
+hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
+  const bool fast = a.vec_state && (a.K % 4) == 0;
+  if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
+#define FORGE_EMBED(FA)                                                                                                \
+  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<FA, O, FMT_BF16, M, V>), tile_grid(a), dim3(NT), 0, st, a, e); \
+  else hipLaunchKernelGGL((k_embed_step<FA, O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a, e);
+  if (fast) { FORGE_EMBED(true) } else { FORGE_EMBED(false) }
+#undef FORGE_EMBED
+  return hipGetLastError();
+}
+#define FORGE_INSTANTIATE_EMBED(O, M, V) \
+  template hipError_t combo_embed<O, M, V>(const KArgs&, const EmbedArgs&, int, hipStream_t);
+
+}  // namespace forge

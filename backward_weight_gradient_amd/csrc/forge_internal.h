@@ -69,6 +69,21 @@ struct KArgs {
   EpiConst c;
 };
 
+// 8-bit activations: codes [rows, K] with pitch ld and dense scale bytes
+// [rows, nb], one per 2^sh columns, nb = ceil(K / 2^sh).
+struct Act8 {
+  uint8_t* codes; int64_t ld;
+  uint8_t* scale;
+  int32_t nb, sh;
+};
+
+// A launch whose X is a.x8 (a.X unused; dY bf16).
+struct KArgs8 : KArgs {
+  Act8 x8;
+  int32_t x_fmt;                  // FMT_S8 / FMT_E4M3
+  int32_t x_dma;                  // dY and the codes qualify for the asynchronous mainloop
+};
+
 // Up to GROUP_MAX independent layers launched together (same formats and
 // optimizer).  first_tile[i] is the first workgroup of layer i;
 // first_tile[n] is the grid size.
@@ -122,6 +137,16 @@ constexpr int WIDE_MIN_BT = 2048;  // token count from which the 256 x 256 kerne
   X(OPT_SGDM, FMT_F32, FMT_NONE)   \
   X(OPT_SGDM, FMT_BF16, FMT_NONE)  \
   X(OPT_SGDM, FMT_E4M3, FMT_NONE)
+// Combinations that also take X in 8 bits.
+#define FORGE_ACT8_LIST(X)         \
+  X(OPT_ADAMW, FMT_F32, FMT_F32)   \
+  X(OPT_ADAMW, FMT_BF16, FMT_BF16) \
+  X(OPT_ADAMW, FMT_S8, FMT_U8)     \
+  X(OPT_ADAMW, FMT_E4M3, FMT_E4M3) \
+  X(OPT_LION, FMT_F32, FMT_NONE)   \
+  X(OPT_LION, FMT_BF16, FMT_NONE)  \
+  X(OPT_SGDM, FMT_F32, FMT_NONE)   \
+  X(OPT_SGDM, FMT_BF16, FMT_NONE)
 #define FORGE_STATE_LIST(X) \
   FORGE_ADAMW_LIST(X) FORGE_LION_LIST(X) FORGE_SGDM_LIST(X) FORGE_ADAM_VARIANT_LIST(X) FORGE_SECOND_MOMENT_LIST(X)
 
@@ -216,6 +241,14 @@ inline bool combo_supported(int in_fmt, int w_fmt, int opt, int m_fmt, int v_fmt
   return false;
 }
 
+inline bool act8_combo_supported(int opt, int m_fmt, int v_fmt) {
+#define X(O, M, V) \
+  if (opt == O && m_fmt == M && v_fmt == V) return true;
+  FORGE_ACT8_LIST(X)
+#undef X
+  return false;
+}
+
 // Whether a layer can run in the grouped kernel (aligned bf16, short token axis).
 inline bool group_eligible(const KArgs& a, int in_fmt) {
   return in_fmt == FMT_BF16 && a.dma_ok && a.vec_state && (a.K % 4) == 0 && a.BT < WIDE_MIN_BT;
@@ -266,5 +299,69 @@ hipError_t launch_debug_quant(const float* in, uint8_t* codes, float* scales, in
 hipError_t launch_debug_copy(const void* src, void* dst, uint64_t bytes, hipStream_t stream);
 hipError_t launch_debug_state_stream(uint16_t* W, float* m, float* v, int N, int K, hipStream_t stream);
 hipError_t launch_debug_mfma(float* out, int blocks, int iters, hipStream_t stream);
+
+
+// forge_k_act8.hip: X (fmt F32 / BF16, [rows, K]) to and from 8 bits.
+hipError_t launch_act_quantize(const void* X, int64_t ldx, int x_fmt, const Act8& q, int q_fmt, int64_t rows, int64_t K,
+                               hipStream_t stream);
+hipError_t launch_act_dequantize(const Act8& q, int q_fmt, void* X, int64_t ldx, int x_fmt, int64_t rows, int64_t K,
+                                 hipStream_t stream);
+// Fused step and accumulation (a.dW = or += G) with X in 8 bits.
+template <int O, int M, int V>
+hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st);
+hipError_t launch_fused_act8(const KArgs8& a, int w_fmt, int opt, int m_fmt, int v_fmt, hipStream_t stream);
+hipError_t launch_gemm_act8(const KArgs8& a, hipStream_t stream);
+
+// forge_k_norm.hip.  Null pointers: absent.
+struct NormArgs {
+  const void* X; int64_t ldx;
+  const void* R; int64_t ldr;
+  const void* gamma;
+  void* H; int64_t ldh;
+  void* Y; int64_t ldy;
+  Act8 q;                          // q.codes null: no 8-bit output
+  float* rstd;
+  int64_t rows; int32_t K;
+  int32_t x_fmt, r_fmt, g_fmt, y_fmt, q_fmt;
+  float eps;
+};
+struct NormBwdArgs {
+  const void* dY; int64_t lddy;
+  const void* H; int64_t ldh;
+  const void* gamma;
+  const float* rstd;
+  const void* dR; int64_t lddr;
+  void* dX; int64_t lddx;
+  float* dgamma;
+  float* ws;                       // [parts, K] partial sums of dgamma
+  int64_t rows; int32_t K;
+  int32_t dy_fmt, h_fmt, g_fmt, dx_fmt;
+  int32_t first, parts;
+};
+int norm_parts(int64_t rows, int64_t K);   // workgroups of the backward kernel
+hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
+hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t stream);
+
+// forge_k_embed.hip.  Tokens sorted by id: key[i], perm[i] (the token), i < T;
+// the tokens of row v are [start[v], end[v]) (both 0 where v does not occur).
+// Padding tokens have key V.
+struct EmbedArgs {
+  const void* ids; int32_t id_bytes;
+  int64_t T, V, K;
+  const void* dY; int64_t lddy; int32_t dy_fmt;
+  float scale;
+  int32_t *key, *perm, *start, *end;
+  uint64_t* part;                  // tokens sorted within parts of embed_part(T)
+};
+inline int64_t embed_part(int64_t T) { return T <= 16384 ? 2048 : 8192; }
+hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
+                        int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t stream);
+hipError_t launch_embed_sort(const EmbedArgs& e, hipStream_t stream);
+hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t stream);
+template <int O, int M, int V>
+hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st);
+// The optimizer step on the embedding's gradient (a: the weight and its state, no X / dY).
+hipError_t launch_embed_step(const KArgs& a, const EmbedArgs& e, int w_fmt, int opt, int m_fmt, int v_fmt,
+                             hipStream_t stream);
 
 }  // namespace forge

@@ -379,6 +379,145 @@ forge_status forge_backward_step_split(const forge_mat* X, const forge_mat* dY, 
                                        forge_mat* dX, void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Activations kept in 8 bits.  X is held from the forward pass to the weight
+ * gradient; as a forge_act8 it takes 1 + 1 / block bytes per element.
+ *
+ * q     : [rows, cols] codes, dtype S8 or E4M3 (OCP E4M3 "fn"), any ld >= cols.
+ * block : 32, 64 or 128 consecutive columns of a row share one scale; the last
+ *         block of a row may be shorter (cols need not be a multiple).
+ * scale : dense row-major [rows, ceil(cols / block)] bytes, the block's
+ *         exponent e plus 127: stored value = code * 2^e.
+ * Encoding: a = max |x| of the block, Q = 127 (S8) or 448 (E4M3); e is the
+ *   smallest integer >= -120 with a <= Q * 2^e, and the code is x * 2^-e rounded
+ *   to nearest, ties to even.  A power of two makes every stored value exact in
+ *   bf16 as well as in fp32, so products on the bf16 matrix cores take the
+ *   stored value itself.  A block with an infinity or a NaN gets the scale byte
+ *   255 and zero codes, and all of it is read as NaN: the failure reaches the
+ *   gradient instead of being clamped away.
+ */
+typedef struct {
+  forge_mat q;
+  uint8_t* scale;
+  int32_t block;
+} forge_act8;
+
+/*
+ * forge_act_quantize -- Q = X in 8 bits.  X: [rows, cols] BF16 or F32; Q: the
+ * same shape, codes and scales written.
+ * forge_act_dequantize -- X = the stored values of Q, BF16 or F32, both exact
+ * (a value that was rounded up past the largest finite number is infinite).
+ * No rows or no columns: a no-op.  rows, cols < 2^31.
+ * Errors: FORGE_E_NULL, E_SHAPE (shapes, block, ld), E_DTYPE, E_ALIGN, E_ALIAS
+ * (codes, scales and X overlap; nothing enqueued) or E_HIP.
+ */
+forge_status forge_act_quantize(const forge_mat* X, forge_act8* Q, void* stream);
+forge_status forge_act_dequantize(const forge_act8* Q, forge_mat* X, void* stream);
+
+/*
+ * forge_wgrad_step_act8 -- forge_wgrad_step with X from its 8-bit copy (paper,
+ * section 2.2 and Algorithm 1): the codes are decoded on their way into the
+ * matrix cores, so G = dY^T (stored values) without X in 16 bits in memory.
+ * The result equals forge_wgrad_step on the decoded BF16 X.
+ * dY: [BT, N] BF16.  W: [N, K] BF16 or F32.  Supported: AdamW with (m, v) in
+ * {(F32, F32), (BF16, BF16), (S8, U8), (E4M3, E4M3)}; Lion and SGD-m with m in
+ * {F32, BF16}.  Any other optimizer: forge_wgrad_accumulate_act8, then
+ * forge_wgrad_step_accumulated with no tokens (BT = 0).
+ * X's block is independent of the states' block.  Other arguments and errors
+ * as forge_wgrad_step, and those of forge_act_dequantize for X.
+ * forge_wgrad_check_act8 -- its validation alone (no device call).
+ * forge_wgrad_accumulate_act8 -- forge_wgrad_accumulate with such an X (and
+ * BF16 dY).
+ */
+forge_status forge_wgrad_step_act8(const forge_act8* X, const forge_mat* dY, forge_mat* W, forge_state* m,
+                                   forge_state* v, const forge_hyper* h, int64_t step, uint64_t seed,
+                                   void* stream);
+forge_status forge_wgrad_check_act8(const forge_act8* X, const forge_mat* dY, const forge_mat* W,
+                                    const forge_state* m, const forge_state* v, const forge_hyper* h,
+                                    int64_t step);
+forge_status forge_wgrad_accumulate_act8(const forge_act8* X, const forge_mat* dY, forge_mat* acc, int32_t first,
+                                         void* stream);
+
+/*
+ * forge_rmsnorm -- root-mean-square norm of each row, with the residual's
+ * addition before it and an 8-bit copy of the output:
+ *   H = X + R (rounded to R's dtype; H = X without R),
+ *   s = 1 / sqrt(mean(H^2) + eps)        (fp32, over the row),
+ *   Y = H s gamma,   Q = the 8-bit copy of the fp32 value of Y.
+ * X     : [rows, cols] BF16 or F32.
+ * R, H  : [rows, cols] BF16 or F32, one dtype; both given or both NULL.  H may be
+ *         R or X itself (same data, ld and dtype), otherwise overlaps nothing.
+ * gamma : [1, cols] F32 or BF16.
+ * Y     : [rows, cols] BF16 (nearest even) or F32, or NULL.
+ * Q     : as forge_act_quantize writes it, or NULL.
+ * rstd  : rows floats (s, which the backward pass reads), or NULL.
+ * eps   : finite, >= 0.  rows, cols < 2^31.
+ * At least one of H, Y, Q, rstd must be given (else E_NULL).  No rows or no
+ * columns: a no-op.
+ * Errors: FORGE_E_NULL, E_SHAPE, E_DTYPE, E_ALIGN, E_HYPER (eps), E_ALIAS
+ * (nothing enqueued) or E_HIP.
+ */
+forge_status forge_rmsnorm(const forge_mat* X, const forge_mat* R, const forge_mat* gamma, double eps, forge_mat* H,
+                           forge_mat* Y, forge_act8* Q, float* rstd, void* stream);
+
+/*
+ * forge_rmsnorm_backward -- with h = a row of H, s = rstd, g = gamma dY:
+ *   dX = s (g - h s mean(g h s)) + dR,
+ *   dgamma = sum over rows of dY h s   (first != 0), or dgamma += that.
+ * dX is the gradient of H: of X and of R alike.
+ * dY     : [rows, cols] BF16 or F32 (forge_dgrad's dX).  H, rstd: as forge_rmsnorm
+ *          left them (H is X where no residual was added).
+ * dR     : [rows, cols] the gradient that reaches H past the norm, dX's dtype, or NULL.
+ * dX     : [rows, cols] BF16 (nearest even) or F32; may be dR or dY itself (same
+ *          data, ld and dtype), otherwise overlaps nothing.  NULL: dgamma alone.
+ * dgamma : cols floats, or NULL: dX alone (no workspace needed).
+ * workspace: forge_rmsnorm_workspace_bytes(rows, cols) bytes, 16-byte aligned
+ *          scratch for dgamma's partial sums, which a second kernel adds in a
+ *          fixed order (the same result from call to call).  Calls that may
+ *          overlap need their own.
+ * No rows: dgamma = 0 or unchanged.  Limits and errors as forge_rmsnorm; E_NULL
+ * / E_SHAPE / E_ALIGN / E_ALIAS for the workspace as forge_dgrad_split.
+ */
+forge_status forge_rmsnorm_backward(const forge_mat* dY, const forge_mat* H, const forge_mat* gamma,
+                                    const float* rstd, const forge_mat* dR, forge_mat* dX, float* dgamma,
+                                    int32_t first, void* workspace, int64_t workspace_bytes, void* stream);
+int64_t forge_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Embedding.  W: [V, K] BF16 or F32.  ids: T token ids, dense int32 or int64
+ * (id_bytes 4 or 8).  An id outside 0 .. V - 1 is padding: its output row is
+ * zero and it has no gradient.
+ *
+ * forge_embed -- Y[t] = scale * W[ids[t]] (fp32, rounded once).  Y: [T, K] BF16
+ * or F32.  T or K 0: a no-op.
+ *
+ * The weight gradient G[v] = scale * sum of dY[t] over the tokens with id v is
+ * made from the tokens sorted by id (stable, on the device), so the sum's order
+ * is fixed and no atomics are used.  dY: [T, K] BF16 or F32.
+ * forge_embed_accumulate -- acc = G (first != 0, every row written) or acc += G
+ * (only the rows that occur are touched).  acc: [V, K] F32.  With
+ * forge_wgrad_step_accumulated as the last micro-step this also covers a weight
+ * that is tied to the output layer.
+ * forge_embed_step -- the optimizer step of forge_wgrad_step on G for every row
+ * of W (rows that do not occur have G = 0), G never in device memory.  W, m, v,
+ * h, step, seed, combinations and limits as forge_wgrad_step.
+ * workspace: forge_embed_workspace_bytes(T, V) bytes, 16-byte aligned scratch.
+ * Calls that may overlap need their own.
+ * T, V, K < 2^31, V * K < 2^32 for the step.  T may be 0 (G = 0).
+ * Errors: FORGE_E_NULL, E_SHAPE (id_bytes, sizes, workspace too small), E_DTYPE,
+ * E_ALIGN, E_HYPER (scale not finite), E_ALIAS, and those of forge_wgrad_step
+ * (nothing enqueued), or E_HIP.
+ */
+forge_status forge_embed(const void* ids, int32_t id_bytes, int64_t T, const forge_mat* W, double scale,
+                         forge_mat* Y, void* stream);
+int64_t forge_embed_workspace_bytes(int64_t T, int64_t V);
+forge_status forge_embed_accumulate(const void* ids, int32_t id_bytes, int64_t T, const forge_mat* dY, double scale,
+                                    forge_mat* acc, int32_t first, void* workspace, int64_t workspace_bytes,
+                                    void* stream);
+forge_status forge_embed_step(const void* ids, int32_t id_bytes, int64_t T, const forge_mat* dY, double scale,
+                              forge_mat* W, forge_state* m, forge_state* v, const forge_hyper* h, int64_t step,
+                              uint64_t seed, void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * forge_wgrad_check -- the validation of forge_wgrad_step alone: same
  * arguments, same return codes, no device call at all (usable on a host
  * without a GPU).

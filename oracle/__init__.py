@@ -15,3 +15,4 @@ readings taken where the pages leave a step open.
 """
 
 from .forge_oracle import *  # noqa: F401,F403
+from .act_oracle import *  # noqa: F401,F403
