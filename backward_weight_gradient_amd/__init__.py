@@ -213,12 +213,17 @@ def mat_raw(ptr: int, dtype: int, rows: int, cols: int, ld: Optional[int] = None
 
 def mat(t) -> forge_mat:
     """A forge_mat describing a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError("expected a 2-D tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError("rows must be contiguous (stride(1) == 1)")
-    ld = t.stride(0) if t.shape[0] > 1 else max(1, t.shape[1])
-    return forge_mat(t.data_ptr() or None, _dtype_code(t), t.shape[0], t.shape[1], ld)
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported tensor dtype {t.dtype}")
+    return forge_mat(t.data_ptr() or None, code, rows, cols, ld if rows > 1 else max(1, cols))
 
 
 def state(t, scale=None, block: int = 0) -> forge_state:
@@ -242,7 +247,7 @@ def state(t, scale=None, block: int = 0) -> forge_state:
 def act8(codes, scale, block: int) -> forge_act8:
     """A forge_act8: int8 or float8_e4m3fn codes [rows, cols] and their uint8 scale
     bytes, a contiguous [rows, ceil(cols / block)] tensor on the codes' device,
-    block in {32, 64, 128}."""
+    block in {32, 64, 128}.  It keeps both tensors alive."""
     if block not in (32, 64, 128):
         raise ValueError(f"act8: block must be 32, 64 or 128, got {block}")
     q = mat(codes)
@@ -250,7 +255,9 @@ def act8(codes, scale, block: int) -> forge_act8:
         raise ValueError("act8: the scale tensor must be contiguous uint8 on the codes' device")
     if scale.numel() != q.rows * -(-q.cols // block):
         raise ValueError(f"act8: {scale.numel()} scales given, {q.rows * -(-q.cols // block)} needed")
-    return forge_act8(q, scale.data_ptr() or None, block)
+    a = forge_act8(q, scale.data_ptr() or None, block)
+    a.tensors = (codes, scale)   # the struct holds addresses only: keep their memory while it lives
+    return a
 
 
 def hyper(opt: str = "adamw", lr: float = 1e-3, beta1: float = 0.9, beta2: Optional[float] = None,
@@ -265,7 +272,6 @@ def hyper(opt: str = "adamw", lr: float = 1e-3, beta1: float = 0.9, beta2: Optio
 
 
 def current_stream() -> int:
-    import torch
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -480,47 +486,39 @@ def forge_wgrad_unfused(X, dY, W, m, v, h: forge_hyper, step: int, seed: int, dW
     return rc
 
 
-class _Launch:
-    """The stream of a call and the device it belongs to: that of its tensors, which
-    need not be the current one.  Tensor arguments must all be on one device;
-    structs made from raw pointers say nothing about theirs."""
-
-    __slots__ = ("device",)
-
-    def __init__(self, *args):
-        self.device = None
-        for a in args:
-            if isinstance(a, torch.Tensor):
-                if self.device is None:
-                    self.device = a.device
-                elif a.device != self.device:
-                    raise ValueError(f"tensors on {self.device} and {a.device} in one call")
-
-    def __call__(self, name, stream, check, fn, *args):
-        d = self.device
-        if d is None or d.type != "cuda" or d.index == torch.cuda.current_device():
-            rc = fn(*args, _stream(stream))
-        else:
-            with torch.cuda.device(d):
-                rc = fn(*args, _stream(stream))
-        if check and rc != FORGE_OK:
-            raise ForgeError(rc, name)
-        return rc
+def _launch(name, stream, check, fn, tensors, *args):
+    """Call fn(*args, stream) on the device of the tensors, which need not be the
+    current one; they must all be on one (structs made from raw pointers say nothing
+    about theirs).  Without a stream: that device's current one."""
+    device = None
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            if device is None:
+                device = t.device
+            elif t.device != device:
+                raise ValueError(f"{name}: tensors on {device} and {t.device} in one call")
+    if device is None or device.type != "cuda" or device.index == torch.cuda.current_device():
+        rc = fn(*args, current_stream() if stream is None else stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, current_stream() if stream is None else stream)
+    if rc != FORGE_OK and check:
+        raise ForgeError(rc, name)
+    return rc
 
 
 def _as_mat(t):
-    return t if t is None or isinstance(t, forge_mat) else mat(t)
+    return mat(t) if isinstance(t, torch.Tensor) else t
 
 
 def _row_mat(t):
     """A 1-D tensor as a [1, n] matrix (a forge_mat or a 2-D tensor as it is)."""
-    if t is None or isinstance(t, forge_mat):
-        return t
-    if t.dim() == 1:
-        if t.numel() > 1 and t.stride(0) != 1:
-            raise ValueError("expected a contiguous vector")
-        return forge_mat(t.data_ptr() or None, _dtype_code(t), 1, t.numel(), max(1, t.numel()))
-    return mat(t)
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        return _as_mat(t)
+    n = t.shape[0]
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError("expected a contiguous vector")
+    return forge_mat(t.data_ptr() or None, _dtype_code(t), 1, n, max(1, n))
 
 
 def _floats(t, n: int, what: str):
@@ -549,19 +547,19 @@ def _ids(ids):
 
 def forge_act_quantize(X, Q: forge_act8, stream=None, check: bool = True) -> int:
     """Q (codes and power-of-two block scales) = X in 8 bits; Q from act8()."""
-    return _Launch(X)("forge_act_quantize", stream, check, lib.forge_act_quantize, _ref(_as_mat(X)), _ref(Q))
+    return _launch("forge_act_quantize", stream, check, lib.forge_act_quantize, (X,), _ref(_as_mat(X)), _ref(Q))
 
 
 def forge_act_dequantize(Q: forge_act8, X, stream=None, check: bool = True) -> int:
     """X (bf16 or float32) = the values Q holds, exactly."""
-    return _Launch(X)("forge_act_dequantize", stream, check, lib.forge_act_dequantize, _ref(Q), _ref(_as_mat(X)))
+    return _launch("forge_act_dequantize", stream, check, lib.forge_act_dequantize, (X,), _ref(Q), _ref(_as_mat(X)))
 
 
 def forge_wgrad_step_act8(X: forge_act8, dY, W, m, v, h: forge_hyper, step: int, seed: int, stream=None,
                           check: bool = True) -> int:
     """forge_wgrad_step with X from its 8-bit copy (dY bf16)."""
-    return _Launch(dY, W)("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, _ref(X),
-                          _ref(_as_mat(dY)), _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed)
+    return _launch("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, (dY, W), _ref(X),
+                   _ref(_as_mat(dY)), _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed)
 
 
 def forge_wgrad_check_act8(X: forge_act8, dY: forge_mat, W: forge_mat, m, v, h: forge_hyper, step: int) -> int:
@@ -570,8 +568,8 @@ def forge_wgrad_check_act8(X: forge_act8, dY: forge_mat, W: forge_mat, m, v, h: 
 
 def forge_wgrad_accumulate_act8(X: forge_act8, dY, acc, first: bool, stream=None, check: bool = True) -> int:
     """forge_wgrad_accumulate with X from its 8-bit copy (dY bf16)."""
-    return _Launch(dY, acc)("forge_wgrad_accumulate_act8", stream, check, lib.forge_wgrad_accumulate_act8, _ref(X),
-                            _ref(_as_mat(dY)), _ref(_as_mat(acc)), 1 if first else 0)
+    return _launch("forge_wgrad_accumulate_act8", stream, check, lib.forge_wgrad_accumulate_act8, (dY, acc), _ref(X),
+                   _ref(_as_mat(dY)), _ref(_as_mat(acc)), 1 if first else 0)
 
 
 def forge_rmsnorm(X, gamma, Y=None, eps: float = 1e-5, R=None, H=None, Q: Optional[forge_act8] = None, rstd=None,
@@ -582,9 +580,9 @@ def forge_rmsnorm(X, gamma, Y=None, eps: float = 1e-5, R=None, H=None, Q: Option
     [rows], kept for forge_rmsnorm_backward.  Every output but one may be None.
     """
     x = _as_mat(X)
-    return _Launch(X, gamma, Y, R, H, rstd)(
-        "forge_rmsnorm", stream, check, lib.forge_rmsnorm, _ref(x), _ref(_as_mat(R)), _ref(_row_mat(gamma)), eps,
-        _ref(_as_mat(H)), _ref(_as_mat(Y)), _ref(Q), _floats(rstd, x.rows, "rstd"))
+    return _launch("forge_rmsnorm", stream, check, lib.forge_rmsnorm, (X, gamma, Y, R, H, rstd), _ref(x),
+                   _ref(_as_mat(R)), _ref(_row_mat(gamma)), eps, _ref(_as_mat(H)), _ref(_as_mat(Y)), _ref(Q),
+                   _floats(rstd, x.rows, "rstd"))
 
 
 def forge_rmsnorm_workspace_bytes(rows: int, cols: int) -> int:
@@ -599,17 +597,17 @@ def forge_rmsnorm_backward(dY, H, gamma, rstd, dX=None, dR=None, dgamma=None, fi
     forge_rmsnorm_workspace_bytes bytes, is needed for dgamma only."""
     h = _as_mat(H)
     ws, nbytes = _workspace(workspace)
-    return _Launch(dY, H, gamma, rstd, dX, dR, dgamma, workspace)(
-        "forge_rmsnorm_backward", stream, check, lib.forge_rmsnorm_backward, _ref(_as_mat(dY)), _ref(h),
-        _ref(_row_mat(gamma)), _floats(rstd, h.rows, "rstd"), _ref(_as_mat(dR)), _ref(_as_mat(dX)),
-        _floats(dgamma, h.cols, "dgamma"), 1 if first else 0, ws, nbytes)
+    return _launch("forge_rmsnorm_backward", stream, check, lib.forge_rmsnorm_backward,
+                   (dY, H, gamma, rstd, dX, dR, dgamma, workspace), _ref(_as_mat(dY)), _ref(h), _ref(_row_mat(gamma)),
+                   _floats(rstd, h.rows, "rstd"), _ref(_as_mat(dR)), _ref(_as_mat(dX)),
+                   _floats(dgamma, h.cols, "dgamma"), 1 if first else 0, ws, nbytes)
 
 
 def forge_embed(ids, W, Y, scale: float = 1.0, stream=None, check: bool = True) -> int:
     """Y[t] = scale * W[ids[t]]; a row of zeros where the id is outside W's rows."""
     ptr, width, T = _ids(ids)
-    return _Launch(ids, W, Y)("forge_embed", stream, check, lib.forge_embed, ptr, width, T, _ref(_as_mat(W)), scale,
-                              _ref(_as_mat(Y)))
+    return _launch("forge_embed", stream, check, lib.forge_embed, (ids, W, Y), ptr, width, T, _ref(_as_mat(W)), scale,
+                   _ref(_as_mat(Y)))
 
 
 def forge_embed_workspace_bytes(T: int, V: int) -> int:
@@ -624,9 +622,8 @@ def forge_embed_accumulate(ids, dY, acc, first: bool, scale: float = 1.0, worksp
     the addition)."""
     ptr, width, T = _ids(ids)
     ws, nbytes = _workspace(workspace)
-    return _Launch(ids, dY, acc, workspace)(
-        "forge_embed_accumulate", stream, check, lib.forge_embed_accumulate, ptr, width, T, _ref(_as_mat(dY)), scale,
-        _ref(_as_mat(acc)), 1 if first else 0, ws, nbytes)
+    return _launch("forge_embed_accumulate", stream, check, lib.forge_embed_accumulate, (ids, dY, acc, workspace), ptr, width,
+                   T, _ref(_as_mat(dY)), scale, _ref(_as_mat(acc)), 1 if first else 0, ws, nbytes)
 
 
 def forge_embed_step(ids, dY, W, m, v, h: forge_hyper, step: int, seed: int, scale: float = 1.0, workspace=None,
@@ -635,9 +632,8 @@ def forge_embed_step(ids, dY, W, m, v, h: forge_hyper, step: int, seed: int, sca
     row of W, in place on W / m / v."""
     ptr, width, T = _ids(ids)
     ws, nbytes = _workspace(workspace)
-    return _Launch(ids, dY, W, workspace)(
-        "forge_embed_step", stream, check, lib.forge_embed_step, ptr, width, T, _ref(_as_mat(dY)), scale,
-        _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed, ws, nbytes)
+    return _launch("forge_embed_step", stream, check, lib.forge_embed_step, (ids, dY, W, workspace), ptr, width, T,
+                   _ref(_as_mat(dY)), scale, _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed, ws, nbytes)
 
 
 def forge_debug_e4m3(inp, out, stream=None, check: bool = True) -> int:

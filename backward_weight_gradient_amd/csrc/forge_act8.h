@@ -67,10 +67,8 @@ __device__ __forceinline__ u32x2 act8_encode(const float (&x)[8], float inv, boo
 template <int FMT>
 __device__ __forceinline__ void act8_decode4(uint32_t w, float f, float* x) {
   if constexpr (FMT == FMT_S8) {
-    // code + 128 as an unsigned byte (one conversion straight from the packed word), minus 128
-    const uint32_t u = w ^ 0x80808080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = ((float)((u >> (8 * i)) & 0xFFu) - 128.f) * f;
+    for (int i = 0; i < 4; ++i) x[i] = (float)(int8_t)((w >> (8 * i)) & 0xFFu) * f;
   } else {
     e4m3_unpack4(w, x);
 #pragma unroll

@@ -69,6 +69,12 @@ forge_status check_act_copy(const forge_act8* Q, const forge_mat* X) {
 void act8_input(const forge_act8* X, KArgs8& a) {
   a.x8 = act8_args(*X);
   a.x_fmt = X->q.dtype == FORGE_S8 ? FMT_S8 : FMT_E4M3;
+  // the asynchronous mainloop: 16-byte aligned rows of dY and 4-byte aligned rows of
+  // codes (a buffer load's alignment), both in whole 16-byte segments, byte offsets
+  // that fit the 32-bit buffer addressing
+  a.x_dma = (vec_ok(a.dY, a.lddy, 8, 2) && a.N % 8 == 0 && vec_ok(X->q.data, X->q.ld, 4, 1) && a.K % 16 == 0 &&
+             (uint64_t)a.BT * (uint64_t)a.lddy * 2 < (1ull << 31) && (uint64_t)a.BT * (uint64_t)X->q.ld < (1ull << 31))
+                ? 1 : 0;
 }
 
 // Token ids: T values of 4 or 8 bytes.

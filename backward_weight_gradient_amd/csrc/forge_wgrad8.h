@@ -73,6 +73,448 @@ struct MainAct8 {
   }
 };
 
+// ------------------------------------------------------------------------
+// Aligned shapes.  dY goes to LDS by the asynchronous loads of the bf16 kernels;
+// X cannot (its bytes have to be decoded), so each thread loads 16 codes and
+// their scale byte of one token into registers D chunks ahead, and writes the 16
+// decoded bf16 into the same swizzled LDS rows two chunks before they are used:
+//   iteration kc:  [wait dY(kc); barrier]  issue dY(kc + S - 1)
+//                  read and multiply chunk kc
+//                  decode X(kc + 2) into stage (kc + 2) % S;  request X(kc + 2 + D)
+// Stage (kc + 2) % S held chunk kc + 2 - S, which every wave is done with at
+// iteration kc's barrier (S >= 3).  X(kc + 2)'s LDS writes are waited for by
+// iteration kc + 1's last fragment wait (lgkmcnt(0)) and seen by all waves after
+// the barrier of iteration kc + 2.  Tokens past the end and loads past the last
+// chunk read as zero (buffer bounds), so every iteration issues the same loads
+// and the waits are constants.
+// ------------------------------------------------------------------------
+
+// 16 codes and the scale byte of one token in flight: one value of five words, so
+// that the byte stays a whole register from its load to its use (as a loop-carried
+// byte of its own the compiler masks it at the top of the loop and waits there).
+typedef uint32_t u32x5 __attribute__((ext_vector_type(5)));
+
+// X's way into LDS.  W: the LDS row's width in features (128 or 256), W / 16
+// threads per token.
+template <int XF, int W>
+struct XStage {
+  __amdgpu_buffer_rsrc_t rC, rS;
+  uint32_t oobC, oobS, offC, offS;   // byte offsets of this thread's codes / scale in token row 0
+  uint32_t ldc, nb;
+  int trow;                          // token within the chunk
+  uint32_t lds;                      // byte offset of the 16 bf16 within an operand region
+  bool fok;                          // the 16 columns are inside the matrix (K % 16 == 0)
+
+  // gtid: thread among the 2 W that fill a 32-token chunk
+  __device__ __forceinline__ void init(const KArgs8& a, int col0, int gtid) {
+    trow = gtid / (W / 16);
+    const int f = 16 * (gtid & (W / 16 - 1));
+    oobC = (uint32_t)((uint64_t)a.BT * a.x8.ld);
+    oobS = (uint32_t)((uint64_t)a.BT * a.x8.nb);
+    rC = make_rsrc(a.x8.codes, oobC);
+    rS = make_rsrc(a.x8.scale, oobS);
+    ldc = (uint32_t)a.x8.ld;
+    nb = (uint32_t)a.x8.nb;
+    fok = col0 + f < a.K;
+    offC = (uint32_t)(col0 + f);
+    offS = (uint32_t)((col0 + f) >> a.x8.sh);
+    lds = (uint32_t)(trow * (W * 2) + ((f * 2) ^ ((trow & 3) << 6)));
+  }
+  __device__ __forceinline__ u32x5 request(const KArgs8& a, int kc) const {
+    const int tok = kc * 32 + trow;
+    const bool in = tok < a.BT && fok;
+    const u32x4 c = __builtin_bit_cast(
+        u32x4, __builtin_amdgcn_raw_buffer_load_b128(rC, in ? (uint32_t)tok * ldc + offC : oobC, 0, 0));
+    const uint32_t s =
+        (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rS, in ? (uint32_t)tok * nb + offS : oobS, 0, 0);
+    return u32x5{c[0], c[1], c[2], c[3], s};
+  }
+  // Codes 4 i .. 4 i + 3 as two words of bf16.
+  __device__ __forceinline__ static u32x2 word(const u32x5& v, int i, float f) {
+    float x[4];
+    act8_decode4<XF>(v[i], f, x);
+    return u32x2{bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3])};
+  }
+  // A 16-byte half of the thread's 32 bytes into the region at `region` (an LDS
+  // byte address).  Inline assembly: the compiler would otherwise wait for the
+  // asynchronous loads to LDS, of which it cannot tell the stage.
+  template <int H>
+  __device__ __forceinline__ void put(uint32_t region, u32x2 lo, u32x2 hi) const {
+    const u32x4 v = {lo[0], lo[1], hi[0], hi[1]};
+    asm volatile("ds_write_b128 %0, %1 offset:%2" ::"v"(region + lds), "v"(v), "i"(16 * H));
+  }
+  // Nothing that uses the loaded words moves above this point (it would wait for
+  // them there).
+  __device__ __forceinline__ static void pin(u32x5& v) { asm volatile("" : "+v"(v)); }
+  __device__ __forceinline__ void store(uint32_t region, const u32x5& v) const {
+    const float f = act8_mul(v[4]);
+    put<0>(region, word(v, 0, f), word(v, 1, f));
+    put<1>(region, word(v, 2, f), word(v, 3, f));
+  }
+};
+
+// dY's half of MainBF16DmaT.
+template <int STAGES>
+struct MainDy {
+  static constexpr int TK = 32, S = STAGES;
+  static constexpr int OPB = TK * TILE * 2, STAGE = 2 * OPB;
+  __amdgpu_buffer_rsrc_t rA;
+  uint32_t oob, base[2];
+  int trow[2], wave;
+  bool fok[2];
+
+  __device__ __forceinline__ void init(const KArgs8& a, int row0) {
+    const int lane = threadIdx.x & 63;
+    wave = threadIdx.x >> 6;
+    oob = (uint32_t)((uint64_t)a.BT * a.lddy * 2);
+    rA = make_rsrc(a.dY, oob);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = 4 * (2 * wave + r) + (lane >> 4);
+      const int c = (lane & 15) ^ ((t & 3) << 2);
+      trow[r] = t;
+      fok[r] = row0 + c * 8 < a.N;
+      base[r] = (uint32_t)(row0 + c * 8) * 2;
+    }
+  }
+  __device__ __forceinline__ void issue(const KArgs8& a, int kc, char* stage) const {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int tok = kc * TK + trow[r];
+      const uint32_t o = (tok < a.BT && fok[r]) ? (uint32_t)tok * (uint32_t)(a.lddy * 2) + base[r] : oob;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void*)(stage + (2 * wave + r) * 1024), 16, o, 0, 0, 0);
+    }
+  }
+};
+
+// Phase 1 for a 256-thread workgroup; acc as dma_accumulate leaves it.  On
+// return no load or LDS access of this wave is outstanding.
+template <int XF, int S, int D>
+struct Act8Loop {
+  using M = MainDy<S>;
+  static_assert(S >= 3 && D == S - 2, "the vmcnt waits count loads for this pair");
+  M ml;
+  XStage<XF, TILE> xs;
+  u32x5 x[D];                        // X(kc + 2 + j) in x[(kc + j) % D] at iteration kc
+  uint32_t lds0, fofsA[2], fofsB[2];
+
+  __device__ __forceinline__ uint32_t region(int k) const { return lds0 + (uint32_t)((k % S) * M::STAGE) + M::OPB; }
+
+  template <int J>
+  __device__ __forceinline__ void iteration(const KArgs8& a, char* ring, int kc, f32x16 (&acc)[2][2]) {
+    bar();
+    ml.issue(a, kc + S - 1, ring + ((kc + S - 1) % S) * M::STAGE);
+    __builtin_amdgcn_sched_barrier(0);
+    const uint32_t cur = lds0 + (uint32_t)((kc % S) * M::STAGE);
+    u32x2 f0[8], f1[8];
+    uint32_t pa[2], pb[2];
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      pa[b] = cur + fofsA[b];
+      pb[b] = cur + fofsB[b];
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f0[2 * b] = tr_read_at<0>(pa[b]);
+      f0[2 * b + 1] = tr_read_at<1024>(pa[b]);
+      f0[4 + 2 * b] = tr_read_at<0>(pb[b]);
+      f0[4 + 2 * b + 1] = tr_read_at<1024>(pb[b]);
+    }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      f1[2 * b] = tr_read_at<4096>(pa[b]);
+      f1[2 * b + 1] = tr_read_at<5120>(pa[b]);
+      f1[4 + 2 * b] = tr_read_at<4096>(pb[b]);
+      f1[4 + 2 * b + 1] = tr_read_at<5120>(pb[b]);
+    }
+    lds_wait<8>(f0);
+#pragma unroll
+    for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < 2; ++bj)
+        acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_join(f0[2 * bi], f0[2 * bi + 1]),
+                                                              frag_join(f0[4 + 2 * bj], f0[4 + 2 * bj + 1]),
+                                                              acc[bi][bj], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    lds_wait<0>(f1);
+#pragma unroll
+    for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < 2; ++bj)
+        acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_join(f1[2 * bi], f1[2 * bi + 1]),
+                                                              frag_join(f1[4 + 2 * bj], f1[4 + 2 * bj + 1]),
+                                                              acc[bi][bj], 0, 0, 0);
+    xs.pin(x[J]);
+    xs.store(region(kc + 2), x[J]);
+    __builtin_amdgcn_sched_barrier(0);
+    x[J] = xs.request(a, kc + 2 + D);
+    __builtin_amdgcn_sched_barrier(0);
+    // dY(kc + 1), which iteration kc + 2 - S = kc - D issued, landed: since then
+    // X(kc + 2) and four loads in each of D iterations (the prologue's dY chunks
+    // have at least as many behind them)
+    wait_vmcnt<4 * D + 2>();
+  }
+
+  template <int... J>
+  __device__ __forceinline__ void sweep(const KArgs8& a, char* ring, int kc, f32x16 (&acc)[2][2],
+                                        std::integer_sequence<int, J...>) {
+    (iteration<J>(a, ring, kc + J, acc), ...);
+  }
+
+  __device__ __forceinline__ void run(const KArgs8& a, char* ring, int row0, int col0, f32x16 (&acc)[2][2]) {
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int wr = wave >> 1, wc = wave & 1;
+    lds0 = (uint32_t)(uintptr_t)(lds_void*)ring;
+#pragma unroll
+    for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < 2; ++bj)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
+    const int nk = (a.BT + M::TK - 1) / M::TK;
+    if (nk == 0) return;
+    const int t = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    const int f = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      fofsA[b] = (uint32_t)MainBF16::off(t, wr * 64 + b * 32 + f);
+      fofsB[b] = (uint32_t)(M::OPB + MainBF16::off(t, wc * 64 + b * 32 + f));
+    }
+    ml.init(a, row0);
+    xs.init(a, col0, tid);
+    u32x5 x0 = xs.request(a, 0), x1 = xs.request(a, 1);
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k) ml.issue(a, k, ring + k * M::STAGE);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < D; ++j) x[j] = xs.request(a, 2 + j);
+    __builtin_amdgcn_sched_barrier(0);
+    xs.store(region(0), x0);
+    xs.store(region(1), x1);
+    // dY(0) landed: the S - 2 later chunks and X(2 .. D + 1) may be in flight
+    wait_vmcnt<2 * (S - 2) + 2 * D>();
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    // (a last sweep past nk multiplies chunks of zeros)
+    for (int kc = 0; kc < nk; kc += D) sweep(a, ring, kc, acc, std::make_integer_sequence<int, D>{});
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
+};
+
+// The occupancy, ring depth and passes in flight of k_fused.
+template <int XF, int OPT, int WF, int MF, int VF, int BLK = 0, bool FULL = false>
+__global__ void __launch_bounds__(NT, (three_per_cu<OPT, WF, MF, VF, true, false, false>() ? 3 : 2))
+    k_fused_act8_dma(const KArgs8 a) {
+  constexpr bool OCC3 = three_per_cu<OPT, WF, MF, VF, true, false, false>();
+  __shared__ __attribute__((aligned(16))) char lds[OCC3 ? LDS_HALF : LDS_BYTES];
+  int ti, tj;
+  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
+  const int row0 = ti * TILE, col0 = tj * TILE;
+  Epilogue<Step<OPT, WF, MF, VF, true, BLK>, FMT_NONE, true, epi_depth<OPT, WF, MF, VF, true, false, false>(), NT, false,
+           FULL> epi;
+  epi.tid = threadIdx.x;
+  constexpr int PRE = epi_pre<OPT, WF, MF, VF, true, false, false>();
+  epi.template prefetch<PRE>(a, row0, col0);
+  f32x16 acc[2][2];
+  Act8Loop<XF, OCC3 ? 3 : 4, OCC3 ? 1 : 2> loop;
+  loop.run(a, lds, row0, col0, acc);
+  bar();   // every wave is done with the stages before G overwrites them
+  if constexpr (OCC3) {
+    epi.template prefetch_rest<PRE>(a, row0, col0);
+    epi.run_halves_rm(a, reinterpret_cast<float*>(lds), acc, row0, col0);
+  } else {
+    store_acc(reinterpret_cast<float*>(lds), acc, threadIdx.x);
+    __syncthreads();
+    epi.run_prefetched_rm(a, reinterpret_cast<const float*>(lds), row0, col0);
+  }
+}
+
+// ------------------------------------------------------------------------
+// Long token axes: wide_accumulate (256 x 256 per workgroup of 8 waves) with X
+// decoded on the way.  Iteration kc decodes X(kc + 1) between the MFMAs of its
+// first k-step into stage (kc + 1) % 4, which held chunk kc - 3; the fragment
+// wait and the barrier between the k-steps make it visible to the second, which
+// reads it.  Two chunks of X are in flight, so the loop is unrolled by two.
+// ------------------------------------------------------------------------
+struct MainWideDy {
+  static constexpr int TK = MainWide::TK, S = MainWide::S, ROWB = MainWide::ROWB;
+  static constexpr int OPB = MainWide::OPB, STAGE = MainWide::STAGE;
+  __amdgpu_buffer_rsrc_t rA;
+  uint32_t oob, base[2];
+  int trow[2], wave;
+  bool fok[2];
+
+  __device__ __forceinline__ void init(const KArgs8& a, int row0) {
+    const int lane = threadIdx.x & 63;
+    wave = threadIdx.x >> 6;
+    oob = (uint32_t)((uint64_t)a.BT * a.lddy * 2);
+    rA = make_rsrc(a.dY, oob);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int t = 2 * (8 * r + wave) + (lane >> 5);
+      const int c = (lane & 31) ^ ((t & 3) << 2);
+      trow[r] = t;
+      fok[r] = row0 + c * 8 < a.N;
+      base[r] = (uint32_t)(row0 + c * 8) * 2;
+    }
+  }
+  template <int R>
+  __device__ __forceinline__ void issue_one(const KArgs8& a, int kc, char* stage) const {
+    const int tok = kc * TK + trow[R];
+    const uint32_t o = (tok < a.BT && fok[R]) ? (uint32_t)tok * (uint32_t)(a.lddy * 2) + base[R] : oob;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rA, (lds_void*)(stage + (8 * R + wave) * 1024), 16, o, 0, 0, 0);
+  }
+};
+
+template <int XF>
+struct Act8Wide {
+  using M = MainWideDy;
+  static constexpr int D = 2;
+  M ml;
+  XStage<XF, MainWide::W> xs;
+  u32x5 x[D];                        // X(kc + 1 + j) in x[(kc + j) % D] at iteration kc
+  uint32_t lds0, off[6], adr[6];
+  u32x2 f0[12], f1[12];
+
+  // MFMA slot I of a k-step: fragment reads as wide_one; FIRST: X's decoding (words
+  // at even slots, their 16-byte writes at slots 3 and 7), else dY's loads.
+  template <bool FIRST, int J, int I>
+  __device__ __forceinline__ void slot(const KArgs8& a, int kc, char* ring, f32x16 (&acc)[4][2], u32x2 (&w)[4], float f) {
+    u32x2 (&cur)[12] = FIRST ? f0 : f1;
+    u32x2 (&nxt)[12] = FIRST ? f1 : f0;
+    constexpr int bi = I >> 1, bj = I & 1, T0 = FIRST ? 16 : 0;
+    acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(frag_join(cur[2 * bi], cur[2 * bi + 1]),
+                                                          frag_join(cur[8 + 2 * bj], cur[8 + 2 * bj + 1]),
+                                                          acc[bi][bj], 0, 0, 0);
+    nxt[I] = tr_read_at<(T0 + 4 * (I & 1)) * M::ROWB>(adr[I >> 1]);
+    if constexpr ((I & 1) == 0) {
+      constexpr int R = 8 + I / 2;
+      nxt[R] = tr_read_at<(T0 + 4 * (R & 1)) * M::ROWB>(adr[4 + ((R - 8) >> 1)]);
+    }
+    if constexpr (FIRST) {
+      if constexpr ((I & 1) == 0) w[I / 2] = xs.word(x[J], I / 2, f);
+      const uint32_t region = lds0 + (uint32_t)(((kc + 1) % M::S) * M::STAGE) + M::OPB;
+      if constexpr (I == 3) xs.template put<0>(region, w[0], w[1]);
+      if constexpr (I == 7) xs.template put<1>(region, w[2], w[3]);
+    } else {
+      if constexpr (I == 0) ml.template issue_one<0>(a, kc + M::S, ring + (kc % M::S) * M::STAGE);
+      if constexpr (I == 4) ml.template issue_one<1>(a, kc + M::S, ring + (kc % M::S) * M::STAGE);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  template <bool FIRST, int J, int... I>
+  __device__ __forceinline__ void kstep(const KArgs8& a, int kc, char* ring, f32x16 (&acc)[4][2],
+                                        std::integer_sequence<int, I...>) {
+    u32x2 w[4];
+    float f = 0.f;
+    if constexpr (FIRST) {
+      xs.pin(x[J]);
+      f = act8_mul(x[J][4]);
+    }
+    (slot<FIRST, J, I>(a, kc, ring, acc, w, f), ...);
+  }
+
+  template <int J>
+  __device__ __forceinline__ void iteration(const KArgs8& a, char* ring, int kc, f32x16 (&acc)[4][2]) {
+    kstep<true, J>(a, kc, ring, acc, std::make_integer_sequence<int, 8>{});
+    x[J] = xs.request(a, kc + 1 + D);
+    __builtin_amdgcn_sched_barrier(0);
+    lds_wait12(f1);
+    // dY(kc + 1), issued by iteration kc - 3, landed: since then X in three iterations
+    // and dY in two (the prologue's loads have at least as many behind them)
+    wait_vmcnt<10>();
+    bar();
+    const uint32_t st = lds0 + (uint32_t)(((kc + 1) % M::S) * M::STAGE);
+#pragma unroll
+    for (int r = 0; r < 6; ++r) adr[r] = st + off[r];
+    kstep<false, J>(a, kc, ring, acc, std::make_integer_sequence<int, 8>{});
+    lds_wait12(f0);
+  }
+
+  __device__ __forceinline__ void run(const KArgs8& a, char* ring, int row0, int col0, f32x16 (&acc)[4][2]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wr = wave >> 2, wc = wave & 3;
+    lds0 = (uint32_t)(uintptr_t)(lds_void*)ring;
+#pragma unroll
+    for (int bi = 0; bi < 4; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < 2; ++bj)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
+    const int nk = (a.BT + M::TK - 1) / M::TK;
+    if (nk == 0) return;
+    const int tl = 8 * (lane >> 5) + ((lane & 15) >> 2);
+    const int fl = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) off[b] = (uint32_t)MainWide::off(tl, wr * 128 + b * 32 + fl);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) off[4 + b] = (uint32_t)(M::OPB + MainWide::off(tl, wc * 64 + b * 32 + fl));
+    ml.init(a, row0);
+    xs.init(a, col0, threadIdx.x);
+    static_assert(M::S == 4 && D == 2, "the vmcnt waits count loads for this pair");
+    u32x5 x0 = xs.request(a, 0);
+#pragma unroll
+    for (int k = 0; k < M::S; ++k) {
+      ml.template issue_one<0>(a, k, ring + k * M::STAGE);
+      ml.template issue_one<1>(a, k, ring + k * M::STAGE);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < D; ++j) x[j] = xs.request(a, 1 + j);
+    __builtin_amdgcn_sched_barrier(0);
+    xs.store(lds0 + M::OPB, x0);
+    wait_vmcnt<10>();   // dY(0) landed: three chunks of dY and two of X behind it
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    bar();
+#pragma unroll
+    for (int r = 0; r < 6; ++r) adr[r] = lds0 + off[r];
+#pragma unroll
+    for (int r = 0; r < 12; ++r)
+      f0[r] = tr_read(adr[r < 8 ? (r >> 1) : 4 + ((r - 8) >> 1)] + (uint32_t)(4 * (r & 1) * M::ROWB));
+    lds_wait12(f0);
+    for (int kc = 0; kc < nk; kc += 2) {   // (a last iteration past nk multiplies zeros)
+      iteration<0>(a, ring, kc, acc);
+      iteration<1>(a, ring, kc + 1, acc);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  }
+};
+
+// As k_fused_wide.
+template <int XF, int OPT, int WF, int MF, int VF, bool FULL>
+__global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_wide(const KArgs8 a) {
+  __shared__ __attribute__((aligned(16))) char lds[LDS_WIDE];
+  const int tw = (a.K + MainWide::W - 1) / MainWide::W;
+  const int mi = (int)blockIdx.x / tw;
+  const int row0 = mi * MainWide::W, col0 = ((int)blockIdx.x - mi * tw) * MainWide::W;
+  f32x16 acc[4][2];
+  Act8Wide<XF> loop;
+  loop.run(a, lds, row0, col0, acc);
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wr = wave >> 2, wc = wave & 3;
+  float* sG = reinterpret_cast<float*>(lds);
+  Epilogue<Step<OPT, WF, MF, VF, true>, FMT_NONE, true, 2, 2 * NT, false, FULL> epi;
+  epi.tid = threadIdx.x;
+  for (int sub = 0; sub < 4; ++sub) {
+    const int srow0 = row0 + (sub >> 1) * TILE, scol0 = col0 + (sub & 1) * TILE;
+    bar();                                   // the ring / the previous sub-tile is no longer read
+    if (wr == (sub >> 1) && (wc >> 1) == (sub & 1)) {
+#pragma unroll
+      for (int bi = 0; bi < 4; ++bi)
+#pragma unroll
+        for (int bj = 0; bj < 2; ++bj)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int r = bi * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+            const int c = (wc & 1) * 64 + bj * 32 + (lane & 31);
+            sG[r * GP + c] = acc[bi][bj][e];
+          }
+    }
+    __syncthreads();
+    if (srow0 < a.N && scol0 < a.K) epi.run_tile_rm(a, sG, srow0, scol0);
+  }
+}
+
+// Any shape.
 template <int OPT, int WF, int MF, int VF>
 __global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
@@ -86,11 +528,44 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
   epi.run_prefetched(a, reinterpret_cast<const float*>(lds), row0, col0);
 }
 
+template <int XF, int O, int M, int V>
+hipError_t fused_act8_dma(const KArgs8& a, int w_fmt, hipStream_t st) {
+#define FORGE_ACT8_DMA(WF, BLK, FULL)                                                                                 \
+  hipLaunchKernelGGL((k_fused_act8_dma<XF, O, WF, M, V, BLK, FULL>), tile_grid(a), dim3(NT), 0, st, a);               \
+  return hipGetLastError();
+  if (a.BT >= WIDE_MIN_BT) {   // (combo_fused's variants)
+    const dim3 g((unsigned)(((a.N + 255) / 256) * ((a.K + 255) / 256)));
+    if constexpr (full_pays(M, V)) {
+      if (whole_tiles(a) && w_fmt == FMT_BF16) {
+        hipLaunchKernelGGL((k_fused_act8_wide<XF, O, FMT_BF16, M, V, true>), g, dim3(2 * NT), 0, st, a);
+        return hipGetLastError();
+      }
+    }
+    if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_fused_act8_wide<XF, O, FMT_BF16, M, V, false>), g, dim3(2 * NT), 0, st, a);
+    else hipLaunchKernelGGL((k_fused_act8_wide<XF, O, FMT_F32, M, V, false>), g, dim3(2 * NT), 0, st, a);
+    return hipGetLastError();
+  }
+  if (w_fmt == FMT_BF16) {
+    // the variants of k_fused that pay with a bf16 weight (combo_fused)
+    if constexpr (fmt_blocked(M)) {
+      if (a.block == 128 && whole_tiles(a)) { FORGE_ACT8_DMA(FMT_BF16, 128, true) }
+    } else if constexpr (full_pays(M, V) && !(M == FMT_F32 && V == FMT_F32)) {
+      if (whole_tiles(a)) { FORGE_ACT8_DMA(FMT_BF16, 0, true) }
+    }
+    FORGE_ACT8_DMA(FMT_BF16, 0, false)
+  }
+  FORGE_ACT8_DMA(FMT_F32, 0, false)
+#undef FORGE_ACT8_DMA
+}
+
 template <int O, int M, int V>
 hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st) {
+  if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
+  if (a.x_dma && a.vec_state && a.K % 4 == 0)
+    return a.x_fmt == FMT_S8 ? fused_act8_dma<FMT_S8, O, M, V>(a, w_fmt, st)
+                             : fused_act8_dma<FMT_E4M3, O, M, V>(a, w_fmt, st);
   if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_fused_act8<O, FMT_BF16, M, V>), tile_grid(a), dim3(NT), 0, st, a);
-  else if (w_fmt == FMT_F32) hipLaunchKernelGGL((k_fused_act8<O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a);
-  else return hipErrorInvalidValue;
+  else hipLaunchKernelGGL((k_fused_act8<O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a);
   return hipGetLastError();
 }
 #define FORGE_INSTANTIATE_ACT8(O, M, V) \
