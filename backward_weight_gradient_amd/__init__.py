@@ -271,7 +271,14 @@ def hyper(opt: str = "adamw", lr: float = 1e-3, beta1: float = 0.9, beta2: Optio
     return forge_hyper(OPTIMIZERS[opt], ROUNDING[round], lr, beta1, beta2, eps, weight_decay)
 
 
+# torch's own accessor of the current stream's handle (no Stream object is made:
+# 0.1 us instead of 2.9), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def current_stream() -> int:
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 

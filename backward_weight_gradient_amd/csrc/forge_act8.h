@@ -76,45 +76,101 @@ __device__ __forceinline__ void act8_decode4(uint32_t w, float f, float* x) {
   }
 }
 
-// 8 elements of a row at column c of type FMT (F32 / BF16) as fp32; columns from
-// K on are 0.  p: the row's element 0.  WHOLE: K % 8 == 0 (or K = 0), so 8 columns
-// are inside or outside together and no element-wise tail is compiled.
+// 8 elements of a row of K at column c, of type FMT (F32 / BF16), as stored.  p: the
+// row's element 0 (a row that exists: callers clamp the row).
+// Loads and their decoding are apart, and neither has a branch that depends on the
+// lane (but the skipped load of WHOLE): a load whose value is used inside such a
+// branch is waited for there, one after another, where several should be in flight.
+//  WHOLE: K % 8 == 0, so 8 columns are inside or outside together; outside is 0.
+//  otherwise: the load is of the 8 elements at min(c, K - 8); row_val8 shifts those
+//    of the vector that K ends in into place and clears columns from K on.  (Rows
+//    shorter than 8 are read element by element: the same for all lanes.)
+template <int FMT> struct Raw8;
+template <> struct Raw8<FMT_F32> { f32x4 a, b; };
+template <> struct Raw8<FMT_BF16> { u32x4 a; };
+
 template <int FMT, bool WHOLE = false>
-__device__ __forceinline__ void row_load8(const void* p, int64_t c, int64_t K, float (&x)[8]) {
-  if constexpr (FMT == FMT_F32) {
-    const float* q = static_cast<const float*>(p) + c;
-    f32x4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
-    if (c + 8 <= K) {
-      a = *reinterpret_cast<const f32x4_u*>(q);
-      b = *reinterpret_cast<const f32x4_u*>(q + 4);
-    } else if constexpr (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (c + i < K) a[i] = q[i];
-        if (c + 4 + i < K) b[i] = q[4 + i];
+__device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t K) {
+  Raw8<FMT> r;
+  if constexpr (FMT == FMT_F32) r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
+  else r.a = u32x4{0u, 0u, 0u, 0u};
+  if constexpr (WHOLE) {
+    if (c < K) {
+      if constexpr (FMT == FMT_F32) {
+        const float* q = static_cast<const float*>(p) + c;
+        r.a = *reinterpret_cast<const f32x4_u*>(q);
+        r.b = *reinterpret_cast<const f32x4_u*>(q + 4);
+      } else {
+        r.a = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(p) + c);
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { x[i] = a[i]; x[4 + i] = b[i]; }
-  } else {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + c;
-    u32x4 a = {0u, 0u, 0u, 0u};
-    if (c + 8 <= K) {
-      a = *reinterpret_cast<const u32x4_u*>(q);
-    } else if constexpr (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < K) a[i >> 1] |= (uint32_t)q[i] << (16 * (i & 1));
+  } else if (K >= 8) {
+    const int64_t at = min(c, K - 8);
+    if constexpr (FMT == FMT_F32) {
+      const float* q = static_cast<const float*>(p) + at;
+      r.a = *reinterpret_cast<const f32x4_u*>(q);
+      r.b = *reinterpret_cast<const f32x4_u*>(q + 4);
+    } else {
+      r.a = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(p) + at);
     }
+  } else {
+    for (int64_t i = K - 1; i >= 0; --i) {   // last element first, each pushing the others up
+      if constexpr (FMT == FMT_F32) {
+        r.b = f32x4{r.a[3], r.b[0], r.b[1], r.b[2]};
+        r.a = f32x4{static_cast<const float*>(p)[i], r.a[0], r.a[1], r.a[2]};
+      } else {
+        r.a = u32x4{(r.a[0] << 16) | static_cast<const uint16_t*>(p)[i], (r.a[1] << 16) | (r.a[0] >> 16),
+                    (r.a[2] << 16) | (r.a[1] >> 16), (r.a[3] << 16) | (r.a[2] >> 16)};
+      }
+    }
+  }
+  return r;
+}
+
+template <int FMT, bool WHOLE = false>
+__device__ __forceinline__ void row_val8(Raw8<FMT> r, int64_t c, int64_t K, float (&x)[8]) {
+  if constexpr (!WHOLE) {
+    // elements the load began too early (rows shorter than 8 begin at 0: nothing to shift for c = 0)
+    const int s = K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
+    if constexpr (FMT == FMT_F32) {
+      const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+      r.a = s & 4 ? r.b : r.a;
+      r.b = s & 4 ? z : r.b;
+      r.a = s & 2 ? f32x4{r.a[2], r.a[3], r.b[0], r.b[1]} : r.a;
+      r.b = s & 2 ? f32x4{r.b[2], r.b[3], 0.f, 0.f} : r.b;
+      r.a = s & 1 ? f32x4{r.a[1], r.a[2], r.a[3], r.b[0]} : r.a;
+      r.b = s & 1 ? f32x4{r.b[1], r.b[2], r.b[3], 0.f} : r.b;
+      r.a = s & 8 ? z : r.a;
+      r.b = s & 8 ? z : r.b;
+    } else {
+      const u32x4 z = {0u, 0u, 0u, 0u};
+      r.a = s & 4 ? u32x4{r.a[2], r.a[3], 0u, 0u} : r.a;
+      r.a = s & 2 ? u32x4{r.a[1], r.a[2], r.a[3], 0u} : r.a;
+      r.a = s & 1 ? u32x4{(r.a[0] >> 16) | (r.a[1] << 16), (r.a[1] >> 16) | (r.a[2] << 16),
+                          (r.a[2] >> 16) | (r.a[3] << 16), r.a[3] >> 16}
+                  : r.a;
+      r.a = s & 8 ? z : r.a;
+    }
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(a[i] << 16);
-      x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (FMT == FMT_F32) {
+      x[i] = r.a[i];
+      x[4 + i] = r.b[i];
+    } else {
+      x[2 * i] = __uint_as_float(r.a[i] << 16);
+      x[2 * i + 1] = __uint_as_float(r.a[i] & 0xFFFF0000u);
     }
   }
 }
 
-// The reverse: 8 values rounded to FMT (nearest even); columns from K on are not written.
+template <int FMT, bool WHOLE = false>
+__device__ __forceinline__ void row_load8(const void* p, int64_t c, int64_t K, float (&x)[8]) {
+  row_val8<FMT, WHOLE>(row_raw8<FMT, WHOLE>(p, c, K), c, K, x);
+}
+
+// The reverse: 8 values rounded to FMT (nearest even); columns from K on are not
+// written (the vector that K ends in: 4, 2 and 1 elements as its length asks).
 template <int FMT, bool WHOLE = false>
 __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const float (&x)[8]) {
   if constexpr (FMT == FMT_F32) {
@@ -122,20 +178,42 @@ __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const 
     if (c + 8 <= K) {
       *reinterpret_cast<f32x4_u*>(q) = f32x4{x[0], x[1], x[2], x[3]};
       *reinterpret_cast<f32x4_u*>(q + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    } else if constexpr (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < K) q[i] = x[i];
+    } else if (!WHOLE && c < K) {
+      const int n = (int)(K - c);
+      float y[4] = {x[0], x[1], x[2], x[3]};
+      if (n & 4) {
+        *reinterpret_cast<f32x4_u*>(q) = f32x4{y[0], y[1], y[2], y[3]};
+        y[0] = x[4]; y[1] = x[5]; y[2] = x[6];
+        q += 4;
+      }
+      if (n & 2) {
+        q[0] = y[0];
+        q[1] = y[1];
+        y[0] = y[2];
+        q += 2;
+      }
+      if (n & 1) q[0] = y[0];
     }
   } else {
     uint16_t* q = static_cast<uint16_t*>(p) + c;
     const u32x4 w = {bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7])};
     if (c + 8 <= K) {
       *reinterpret_cast<u32x4_u*>(q) = w;
-    } else if constexpr (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < K) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    } else if (!WHOLE && c < K) {
+      const int n = (int)(K - c);
+      uint32_t y0 = w[0], y1 = w[1];
+      if (n & 4) {
+        *reinterpret_cast<u32x2_e*>(q) = u32x2_e{y0, y1};
+        y0 = w[2];
+        y1 = w[3];
+        q += 4;
+      }
+      if (n & 2) {
+        *reinterpret_cast<u32_e*>(q) = y0;
+        y0 = y1;
+        q += 2;
+      }
+      if (n & 1) q[0] = (uint16_t)y0;
     }
   }
 }
@@ -143,21 +221,38 @@ __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const 
 // Store 8 codes of a row; columns from K on are not written.
 template <bool WHOLE = false>
 __device__ __forceinline__ void codes_store8(uint8_t* p, int64_t c, int64_t K, u32x2 w) {
+  uint8_t* q = p + c;
   if (c + 8 <= K) {
-    *reinterpret_cast<u32x2_u*>(p + c) = w;
-  } else if constexpr (!WHOLE) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c + i < K) p[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+    *reinterpret_cast<u32x2_u*>(q) = w;
+  } else if (!WHOLE && c < K) {
+    const int n = (int)(K - c);
+    uint32_t y = w[0];
+    if (n & 4) {
+      *reinterpret_cast<u32_e*>(q) = y;
+      y = w[1];
+      q += 4;
+    }
+    if (n & 2) {
+      q[0] = (uint8_t)y;
+      q[1] = (uint8_t)(y >> 8);
+      y >>= 16;
+      q += 2;
+    }
+    if (n & 1) q[0] = (uint8_t)y;
   }
 }
-__device__ __forceinline__ u32x2 codes_load8(const uint8_t* p, int64_t c, int64_t K) {
-  if (c + 8 <= K) return *reinterpret_cast<const u32x2_u*>(p + c);
+// 8 codes at column c, the same way: the load, then codes_val8.
+__device__ __forceinline__ u32x2 codes_raw8(const uint8_t* p, int64_t c, int64_t K) {
+  if (K >= 8) return *reinterpret_cast<const u32x2_u*>(p + min(c, K - 8));
   u32x2 w = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (c + i < K) w[i >> 2] |= (uint32_t)p[c + i] << (8 * (i & 3));
+  for (int64_t i = K - 1; i >= 0; --i) w = u32x2{(w[0] << 8) | p[i], (w[1] << 8) | (w[0] >> 24)};
   return w;
+}
+__device__ __forceinline__ u32x2 codes_val8(u32x2 w, int64_t c, int64_t K) {
+  const int s = K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
+  const uint32_t lo = s & 4 ? w[1] : w[0], hi = s & 4 ? 0u : w[1];
+  const u32x2 v = {__builtin_amdgcn_alignbyte(hi, lo, s & 3), hi >> (8 * (s & 3))};
+  return s & 8 ? u32x2{0u, 0u} : v;
 }
 
 // Quantise and store the 8 values at column c of row r, the lane's share of a

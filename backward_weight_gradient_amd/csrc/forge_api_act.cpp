@@ -107,11 +107,10 @@ forge_status check_embed_grad(const void* ids, int32_t id_bytes, int64_t T, cons
   e.dY = dY->data; e.lddy = dY->ld; e.dy_fmt = dY->dtype;
   e.scale = (float)scale;
   char* p = static_cast<char*>(ws);
-  e.part = reinterpret_cast<uint64_t*>(p);  p += round16(8 * T);
   e.key = reinterpret_cast<int32_t*>(p);    p += round16(4 * T);
   e.perm = reinterpret_cast<int32_t*>(p);   p += round16(4 * T);
-  e.start = reinterpret_cast<int32_t*>(p);  p += round16(4 * (V + 1));
-  e.end = reinterpret_cast<int32_t*>(p);
+  e.tile = reinterpret_cast<int32_t*>(p);   p += round16(4 * (V / EMBED_MIN_ROWS + 2));
+  e.part = reinterpret_cast<uint64_t*>(p);
   return FORGE_OK;
 }
 
@@ -287,7 +286,7 @@ forge_status forge_embed(const void* ids, int32_t id_bytes, int64_t T, const for
 
 int64_t forge_embed_workspace_bytes(int64_t T, int64_t V) {
   if (T < 0 || V <= 0 || T >= kMax31 || V >= kMax31 - 1) return 0;
-  return round16(8 * T) + 2 * round16(4 * T) + 2 * round16(4 * (V + 1));
+  return 2 * round16(4 * T) + round16(4 * (V / EMBED_MIN_ROWS + 2)) + (T > EMBED_PART ? 8 * T : 0);
 }
 
 forge_status forge_embed_accumulate(const void* ids, int32_t id_bytes, int64_t T, const forge_mat* dY, double scale,

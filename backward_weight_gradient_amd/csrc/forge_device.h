@@ -935,6 +935,12 @@ template <typename T> __device__ __forceinline__ void st_nt(void* p, T v) {
   __builtin_nontemporal_store(v, reinterpret_cast<T*>(p));
 }
 
+// 4 elements at any element alignment (gfx950 takes vector accesses of global memory
+// at any byte address).
+typedef float f32x4_e __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x2_e __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_e __attribute__((aligned(1)));
+
 // Element offsets of one thread's segment in the current pass.
 //  FAST: rows allow aligned 4-element vector accesses and K % 4 == 0, so a
 //        segment is either entirely inside the matrix or entirely outside;
@@ -979,6 +985,26 @@ __device__ __forceinline__ void ld4(Raw4<FMT>& r, const void* seg, const Seg& g,
       r.v = e[0] | (e[1] << 8) | (e[2] << 16) | (e[3] << 24);
     }
   }
+}
+
+// The same for rows of any alignment and length K >= 4 (the ANY steps): one vector
+// access in any case, the segment that the row ends in read 4 - nv elements early
+// and shifted down by any_shift4 once it is decoded.  (With element-wise reads the
+// branches make each segment wait for its own loads.)  8-bit rows are whole blocks.
+template <int FMT>
+__device__ __forceinline__ void ld4_any(Raw4<FMT>& r, const void* seg, const Seg& g) {
+  const int early = 4 - g.nv;
+  if constexpr (FMT == FMT_F32) r.v = ld_nt<f32x4_e>(static_cast<const float*>(seg) - early);
+  else if constexpr (FMT == FMT_BF16) r.v = ld_nt<u32x2_e>(static_cast<const uint16_t*>(seg) - early);
+  else if constexpr (fmt_blocked(FMT)) r.v = ld_nt<u32_e>(seg);
+}
+__device__ __forceinline__ void any_shift4(float* x, const Seg& g) {
+  const int early = 4 - g.nv;
+  x[0] = early & 2 ? x[2] : x[0];
+  x[1] = early & 2 ? x[3] : x[1];
+  x[0] = early & 1 ? x[1] : x[0];
+  x[1] = early & 1 ? x[2] : x[1];
+  x[2] = early & 1 ? x[3] : x[2];
 }
 
 template <int FMT>
@@ -1038,12 +1064,14 @@ __device__ __forceinline__ void dec4_codes(const Raw4<FMT>& r, float* x) {
 // bf16: stochastic rounding when sr is all ones (idx = flat index of the
 // first element), round to nearest even when it is zero.  FAST segments
 // start at an even flat index (K % 4 == 0), so they are two hash pairs.
-template <int FMT, bool FAST, int RM = RM_SEL>
+template <int FMT, bool FAST, int RM = RM_SEL, bool ANY = false>
 __device__ __forceinline__ void st4(void* seg, const Seg& g, bool vec, const float* x, uint32_t sr, uint32_t key,
                                     uint32_t idx) {
   if constexpr (FMT == FMT_F32) {
     float* p = static_cast<float*>(seg);
-    if (FAST || (vec && g.nv == 4)) {
+    if (ANY && g.nv == 4) {
+      st_nt<f32x4_e>(p, f32x4_e{x[0], x[1], x[2], x[3]});
+    } else if (FAST || (vec && g.nv == 4)) {
       st_nt<f32x4>(p, f32x4{x[0], x[1], x[2], x[3]});
     } else {
 #pragma unroll
@@ -1072,7 +1100,9 @@ __device__ __forceinline__ void st4(void* seg, const Seg& g, bool vec, const flo
       hi = bf16x2_select(x[2], x[3], sr_elem_word(key, idx + 2u), sr_elem_word(key, idx + 3u), sr);
     }
     uint16_t* p = static_cast<uint16_t*>(seg);
-    if (FAST || (vec && g.nv == 4)) {
+    if (ANY && g.nv == 4) {
+      st_nt<u32x2_e>(p, u32x2_e{lo, hi});
+    } else if (FAST || (vec && g.nv == 4)) {
       st_nt<u32x2>(p, u32x2{lo, hi});
     } else {
       const uint32_t b[4] = {lo & 0xFFFFu, lo >> 16, hi & 0xFFFFu, hi >> 16};
@@ -1267,8 +1297,10 @@ __device__ __forceinline__ const char* at(const char* base, int64_t pass, O off,
 }
 
 // BLK: the 8-bit block size when fixed at compile time (0: a.block at run time).
-template <int OPT, int WF, int MF, int VF, bool FAST, int BLK = 0>
+// ANY: rows of any alignment, at least 4 elements long (not with FAST).
+template <int OPT, int WF, int MF, int VF, bool FAST, int BLK = 0, bool ANY = false>
 struct Step {
+  static_assert(!(FAST && ANY), "one or the other");
   static_assert(BLK == 0 || BLK == 32 || BLK == 64 || BLK == 128, "block of 32, 64 or 128");
   static constexpr int FIXED_BLOCK = BLK;
   static constexpr bool HAS_M = opt_has_m(OPT);
@@ -1289,6 +1321,12 @@ struct Step {
 
   static constexpr int esz(int fmt) { return fmt == FMT_F32 ? 4 : fmt == FMT_BF16 ? 2 : 1; }
 
+  template <int FMT>
+  __device__ __forceinline__ static void read4(Raw4<FMT>& r, const void* seg, const Seg& g, bool vec) {
+    if constexpr (ANY) ld4_any<FMT>(r, seg, g);
+    else ld4<FMT, FAST>(r, seg, g, vec);
+  }
+
   __device__ __forceinline__ static void load(const KArgs& a, const TileRows<FAST>& tr, int s, const Seg (&sg)[2],
                                               Pending& r) {
     const bool vec = a.vec_state != 0;
@@ -1298,16 +1336,16 @@ struct Step {
         zero4(r.w[g]); zero4(r.m[g]); zero4(r.v[g]);
         continue;
       }
-      ld4<WF, FAST>(r.w[g], at(tr.w, s * tr.dw, tr.ow, 64 * g * esz(WF)), sg[g], vec);
+      read4<WF>(r.w[g], at(tr.w, s * tr.dw, tr.ow, 64 * g * esz(WF)), sg[g], vec);
       if constexpr (fmt_blocked(WF))
         r.w[g].s = *reinterpret_cast<const float*>(at(tr.ws, s * tr.ds, tr.os, g * tr.s1));
       if constexpr (HAS_M) {
-        ld4<MF, FAST>(r.m[g], at(tr.m, s * tr.dm, tr.om, 64 * g * esz(MF)), sg[g], vec);
+        read4<MF>(r.m[g], at(tr.m, s * tr.dm, tr.om, 64 * g * esz(MF)), sg[g], vec);
         if constexpr (fmt_blocked(MF))
           r.m[g].s = *reinterpret_cast<const float*>(at(tr.ms, s * tr.ds, tr.os, g * tr.s1));
       }
       if constexpr (HAS_V) {
-        ld4<VF, FAST>(r.v[g], at(tr.v, s * tr.dv, tr.ov, 64 * g * esz(VF)), sg[g], vec);
+        read4<VF>(r.v[g], at(tr.v, s * tr.dv, tr.ov, 64 * g * esz(VF)), sg[g], vec);
         if constexpr (fmt_blocked(VF))
           r.v[g].s = *reinterpret_cast<const float*>(at(tr.vs, s * tr.ds, tr.os, g * tr.s1));
       }
@@ -1388,6 +1426,11 @@ struct Step {
       } else {
         dec4<VFMT>(r.v[s], v + 4 * s);
       }
+      if constexpr (ANY) {
+        any_shift4(w + 4 * s, sg[s]);
+        any_shift4(m + 4 * s, sg[s]);
+        any_shift4(v + 4 * s, sg[s]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) phi(FOLD_M || FOLD_V ? kc[i >> 2] : a.c, g[i], w[i], m[i], v[i]);
@@ -1398,13 +1441,13 @@ struct Step {
       if (!sg[s].ok) continue;
       const uint32_t idx = rowbase + tr.qg[s];
       if constexpr (!fmt_blocked(WF))
-        st4<WF, FAST, RM>(at(tr.w, ps * tr.dw, tr.ow, 64 * s * esz(WF)), sg[s], vec, w + 4 * s, a.c.sr, a.c.keyW,
+        st4<WF, FAST, RM, ANY>(at(tr.w, ps * tr.dw, tr.ow, 64 * s * esz(WF)), sg[s], vec, w + 4 * s, a.c.sr, a.c.keyW,
                       idx);
       if constexpr (HAS_M && !fmt_blocked(MF))
-        st4<MF, FAST, RM>(at(tr.m, ps * tr.dm, tr.om, 64 * s * esz(MF)), sg[s], vec, m + 4 * s, a.c.sr, a.c.keyM,
+        st4<MF, FAST, RM, ANY>(at(tr.m, ps * tr.dm, tr.om, 64 * s * esz(MF)), sg[s], vec, m + 4 * s, a.c.sr, a.c.keyM,
                       idx);
       if constexpr (HAS_V && !fmt_blocked(VF))
-        st4<VF, FAST, RM>(at(tr.v, ps * tr.dv, tr.ov, 64 * s * esz(VF)), sg[s], vec, v + 4 * s, a.c.sr, a.c.keyV,
+        st4<VF, FAST, RM, ANY>(at(tr.v, ps * tr.dv, tr.ov, 64 * s * esz(VF)), sg[s], vec, v + 4 * s, a.c.sr, a.c.keyV,
                       idx);
     }
     // a block-scaled stream: segment pointers of the codes (1 byte each) and of the scales
@@ -1448,10 +1491,11 @@ struct Step {
 // N and K are multiples of the tile), so every segment is in bounds at
 // compile time and the per-segment checks, and the branches around the
 // loads, stores and block reductions they guard, fold away.
-template <class S, int GF, bool FAST, int DEPTH, int NTE = NT, bool ACC = false, bool FULL = false>
+// ROWS: rows of the tile (a multiple of a pass's).
+template <class S, int GF, bool FAST, int DEPTH, int NTE = NT, bool ACC = false, bool FULL = false, int ROWS = TILE>
 struct Epilogue {
   static_assert(!ACC || GF == FMT_NONE, "the accumulator adds to the staged tile");
-  static constexpr int PASSES = TILE * TILE / (8 * NTE);  // 8 with 256 threads, 4 with 512
+  static constexpr int PASSES = ROWS * TILE / (8 * NTE);  // of 128 rows: 8 with 256 threads, 4 with 512
   static constexpr int RPP = NTE / 16;                    // rows per pass
   static constexpr int GR = ACC ? FMT_F32 : GF;           // format of the G words loaded per pass
   typename S::Pending pend[DEPTH];

@@ -6,12 +6,12 @@
 
 namespace forge {
 
-// G tile (128 rows of W from row0, 128 columns from col0) into LDS:
+// G tile (ROWS rows of W from row0, 128 columns from col0) into LDS:
 //   sG[r * GP + c] = scale * sum over the tokens of row row0 + r of dY[token][col0 + c].
-// 16 lanes of 8 columns per token.  A row of up to LONG_ROW tokens belongs to one
-// wave, 4 tokens at a time; a longer one to the whole workgroup, 16 at a time.
-// Sums over a slot's tokens in order, then over the slots in a fixed order.
-// red: 3 x 128 floats.
+// first, last: the tile's places among the sorted tokens.  16 lanes of 8 columns per
+// token.  A row of up to LONG_ROW tokens belongs to one wave, 4 tokens at a time; a
+// longer one to the whole workgroup, 16 at a time.  Sums over a slot's tokens in
+// order, then over the slots in a fixed order.  rng: 2 ROWS ints, red: 3 x 128 floats.
 constexpr int LONG_ROW = 32;
 
 template <int DF>
@@ -19,7 +19,7 @@ __device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int
   constexpr int ds = DF == FMT_F32 ? 4 : 2;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s[k] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = first; i < n; i += step) {
     float x[8];
     row_load8<DF>(static_cast<const char*>(e.dY) + (int64_t)e.perm[i] * e.lddy * ds, c, e.K, x);
@@ -33,26 +33,33 @@ __device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int
   }
 }
 
-template <int DF>
-__device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* rng, float* red, int row0, int col0) {
+template <int DF, int ROWS>
+__device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* rng, float* red, int row0, int col0, int first,
+                                           int last) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cl = 8 * (lane & 15);
   const int64_t c = (int64_t)col0 + cl;
-  if (tid < TILE) {
-    const bool in = (int64_t)row0 + tid < e.V;
-    rng[2 * tid] = in ? e.start[row0 + tid] : 0;
-    rng[2 * tid + 1] = in ? e.end[row0 + tid] : 0;
+  for (int i = tid; i < ROWS * GP / 4; i += NT) reinterpret_cast<f32x4*>(sG)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (first >= last) {     // (the same for the whole workgroup)
+    __syncthreads();
+    return;
   }
-  for (int i = tid; i < TILE * GP / 4; i += NT) reinterpret_cast<f32x4*>(sG)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < 2 * ROWS; i += NT) rng[i] = 0;
+  __syncthreads();
+  for (int p = first + tid; p < last; p += NT) {
+    const int k = e.key[p];
+    if (p == first || e.key[p - 1] != k) rng[2 * (k - row0)] = p;
+    if (p + 1 == last || e.key[p + 1] != k) rng[2 * (k - row0) + 1] = p + 1;
+  }
   __syncthreads();
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = half * 64 + lane;
-    const int n = rng[2 * r + 1] - rng[2 * r];
+  for (int base = 0; base < ROWS; base += 64) {
+    const int r = base + lane;
+    const int n = r < ROWS ? rng[2 * r + 1] - rng[2 * r] : 0;
     // rows of this wave (r % 4 == wave) with few tokens, then the long rows with all waves
     uint64_t mine = __ballot(n > 0 && n <= LONG_ROW && (r & 3) == wave), all = __ballot(n > LONG_ROW);
     while (mine) {
-      const int k = half * 64 + __builtin_ctzll(mine);
+      const int k = base + __builtin_ctzll(mine);
       mine &= mine - 1;
       float s[8];
       gather_tokens<DF>(e, rng[2 * k] + (lane >> 4), rng[2 * k + 1], 4, c, s);
@@ -62,7 +69,7 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
       }
     }
     while (all) {   // the same rows in every wave
-      const int k = half * 64 + __builtin_ctzll(all);
+      const int k = base + __builtin_ctzll(all);
       all &= all - 1;
       float s[8];
       gather_tokens<DF>(e, rng[2 * k] + (tid >> 4), rng[2 * k + 1], 16, c, s);
@@ -83,32 +90,48 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
   __syncthreads();
 }
 
-template <bool FAST, int OPT, int WF, int MF, int VF>
+// ANY: rows of any alignment, at least 4 elements long.
+template <int ROWS, bool FAST, bool ANY, int OPT, int WF, int MF, int VF>
 __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const EmbedArgs e) {
-  __shared__ __attribute__((aligned(16))) float sG[TILE * GP];
-  __shared__ int rng[2 * TILE];
+  __shared__ __attribute__((aligned(16))) float sG[ROWS * GP];
+  __shared__ int rng[2 * ROWS];
   __shared__ float red[3 * TILE];
-  int ti, tj;
-  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
-  const int row0 = ti * TILE, col0 = tj * TILE;
-  Epilogue<Step<OPT, WF, MF, VF, FAST>, FMT_NONE, FAST, 4> epi;
+  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  const int row0 = ti * ROWS, col0 = tj * TILE;
+  Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, ROWS> epi;
   epi.tid = threadIdx.x;
   epi.prefetch(a, row0, col0);
-  if (e.dy_fmt == FMT_F32) embed_tile<FMT_F32>(e, sG, rng, red, row0, col0);
-  else embed_tile<FMT_BF16>(e, sG, rng, red, row0, col0);
+  const int first = e.T ? e.tile[ti] : 0, last = e.T ? e.tile[ti + 1] : 0;
+  if (e.dy_fmt == FMT_F32) embed_tile<FMT_F32, ROWS>(e, sG, rng, red, row0, col0, first, last);
+  else embed_tile<FMT_BF16, ROWS>(e, sG, rng, red, row0, col0, first, last);
   epi.run_prefetched(a, sG, row0, col0);
 }
 
+// Tiles of 128 rows, or of 16 where those would be fewer than two per CU: then a
+// step is bound by the gathering of each tile's tokens, not by HBM.
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
   const bool fast = a.vec_state && (a.K % 4) == 0;
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
-#define FORGE_EMBED(FA)                                                                                                \
-  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<FA, O, FMT_BF16, M, V>), tile_grid(a), dim3(NT), 0, st, a, e); \
-  else hipLaunchKernelGGL((k_embed_step<FA, O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a, e);
-  if (fast) { FORGE_EMBED(true) } else { FORGE_EMBED(false) }
-#undef FORGE_EMBED
+  const int64_t rows = (int64_t)a.tiles_n * a.tiles_k >= 512 && a.K >= 4 ? TILE : EMBED_MIN_ROWS;
+  const int64_t tiles = (a.N + rows - 1) / rows;
+  if (e.T > 0) {
+    const hipError_t err = launch_embed_tiles(e, rows, tiles, st);
+    if (err != hipSuccess) return err;
+  }
+  const dim3 grid((unsigned)(tiles * a.tiles_k));
+#define FORGE_EMBED(ROWS, FA, ANY)                                                                                          \
+  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<ROWS, FA, ANY, O, FMT_BF16, M, V>), grid, dim3(NT), 0, st, a, e); \
+  else hipLaunchKernelGGL((k_embed_step<ROWS, FA, ANY, O, FMT_F32, M, V>), grid, dim3(NT), 0, st, a, e);                    \
   return hipGetLastError();
+  if (rows == TILE) {
+    if (fast) { FORGE_EMBED(TILE, true, false) }
+    FORGE_EMBED(TILE, false, true)
+  }
+  if (fast) { FORGE_EMBED(EMBED_MIN_ROWS, true, false) }
+  if (a.K >= 4) { FORGE_EMBED(EMBED_MIN_ROWS, false, true) }
+  FORGE_EMBED(EMBED_MIN_ROWS, false, false)
+#undef FORGE_EMBED
 }
 #define FORGE_INSTANTIATE_EMBED(O, M, V) \
   template hipError_t combo_embed<O, M, V>(const KArgs&, const EmbedArgs&, int, hipStream_t);

@@ -342,21 +342,23 @@ int norm_parts(int64_t rows, int64_t K);   // workgroups of the backward kernel
 hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t stream);
 hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t stream);
 
-// forge_k_embed.hip.  Tokens sorted by id: key[i], perm[i] (the token), i < T;
-// the tokens of row v are [start[v], end[v]) (both 0 where v does not occur).
-// Padding tokens have key V.
+// forge_k_embed.hip.  Tokens sorted by id: key[i] (the row), perm[i] (the token), i < T.
+// Padding tokens have key V and so come last.
+constexpr int EMBED_PART = 8192;   // tokens sorted together in LDS
+constexpr int EMBED_MIN_ROWS = 16; // rows of the step's smaller tiles
 struct EmbedArgs {
   const void* ids; int32_t id_bytes;
   int64_t T, V, K;
   const void* dY; int64_t lddy; int32_t dy_fmt;
   float scale;
-  int32_t *key, *perm, *start, *end;
-  uint64_t* part;                  // tokens sorted within parts of embed_part(T)
+  int32_t *key, *perm;
+  int32_t* tile;                   // the step: where each tile's rows begin among the sorted tokens
+  uint64_t* part;                  // T > EMBED_PART: tokens sorted within their parts
 };
-inline int64_t embed_part(int64_t T) { return T <= 16384 ? 2048 : 8192; }
 hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
                         int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t stream);
 hipError_t launch_embed_sort(const EmbedArgs& e, hipStream_t stream);
+hipError_t launch_embed_tiles(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t stream);
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t stream);
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st);

@@ -32,22 +32,19 @@ __device__ __forceinline__ void quantize_unit(const ActArgs& a, int64_t unit) {
   const int tpr = 1 << a.tsh, rpb = NT >> a.tsh;
   const int64_t c = ((int64_t)seg * tpr + (threadIdx.x & (tpr - 1))) * 8;
   const int64_t r0 = rb * (rpb * ACT_UNR) + (threadIdx.x >> a.tsh);
-  float x[ACT_UNR][8];
   constexpr int es = XF == FMT_F32 ? 4 : 2;
+  Raw8<XF> w[ACT_UNR];
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
-    const int64_t r = r0 + (int64_t)u * rpb;
-    if (r < a.rows && c < a.K) {
-      row_load8<XF>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K, x[u]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-    }
+    const int64_t r = min(r0 + (int64_t)u * rpb, a.rows - 1);   // a row past the end: read again, not stored
+    w[u] = row_raw8<XF>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K);
   }
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = r0 + (int64_t)u * rpb;
-    act8_store8<QF>(a.q, r, r < a.rows ? c : a.K, a.K, x[u]);
+    float x[8];
+    row_val8<XF>(w[u], c, a.K, x);
+    act8_store8<QF>(a.q, r, r < a.rows ? c : a.K, a.K, x);
   }
 }
 
@@ -59,25 +56,24 @@ __device__ __forceinline__ void dequantize_unit(const ActArgs& a, int64_t unit) 
   const int64_t c = ((int64_t)seg * tpr + (threadIdx.x & (tpr - 1))) * 8;
   const int64_t r0 = rb * (rpb * ACT_UNR) + (threadIdx.x >> a.tsh);
   if (c >= a.K) return;
+  constexpr int es = XF == FMT_F32 ? 4 : 2;
   u32x2 w[ACT_UNR];
   uint32_t s[ACT_UNR];
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
-    const int64_t r = r0 + (int64_t)u * rpb;
-    if (r < a.rows) {
-      w[u] = codes_load8(a.q.codes + r * a.q.ld, c, a.K);
-      s[u] = a.q.scale[r * a.q.nb + (c >> a.q.sh)];
-    }
+    const int64_t r = min(r0 + (int64_t)u * rpb, a.rows - 1);
+    w[u] = codes_raw8(a.q.codes + r * a.q.ld, c, a.K);
+    s[u] = a.q.scale[r * a.q.nb + (c >> a.q.sh)];
   }
-  constexpr int es = XF == FMT_F32 ? 4 : 2;
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = r0 + (int64_t)u * rpb;
     if (r >= a.rows) return;
     float x[8];
     const float f = act8_mul(s[u]);
-    act8_decode4<QF>(w[u][0], f, x);
-    act8_decode4<QF>(w[u][1], f, x + 4);
+    const u32x2 v = codes_val8(w[u], c, a.K);
+    act8_decode4<QF>(v[0], f, x);
+    act8_decode4<QF>(v[1], f, x + 4);
     row_store8<XF>(static_cast<char*>(a.Xo) + r * a.ldx * es, c, a.K, x);
   }
 }

@@ -88,6 +88,15 @@ __device__ __forceinline__ void add_residual8(const NormArgs& a, int64_t row, in
   row_store8<RF, WHOLE>(static_cast<char*>(a.H) + row * a.ldh * (RF == FMT_F32 ? 4 : 2), c, lim, h);
 }
 
+// A row that needs VEC vectors ends in the last of them: f<whole>(j) with whole = true
+// for the others.
+template <bool WHOLE, int VEC, class F>
+__device__ __forceinline__ void each_vector(F&& f) {
+#pragma unroll
+  for (int j = 0; j + 1 < VEC; ++j) f(std::true_type{}, j);
+  f(std::integral_constant<bool, WHOLE>{}, VEC - 1);
+}
+
 // RF: the residual's format, FMT_NONE without one.
 template <int XF, int RF, int LPR, int VEC, bool WHOLE>
 __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a) {
@@ -97,25 +106,31 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
   const int i = threadIdx.x & (LPR - 1);
   const int64_t K = a.K;
   float gam[VEC][8];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) load8_as<WHOLE>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
+  each_vector<WHOLE, VEC>([&](auto w, int j) {
+    load8_as<w()>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
+  });
   int buf = 0;
   for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB, buf ^= 1) {
-    const int64_t row = base + threadIdx.x / LPR;
+    const int64_t row = base + threadIdx.x / LPR, rd = min(row, a.rows - 1);
     const bool live = row < a.rows;
-    const int64_t lim = live ? K : 0;     // a row past the end loads and stores nothing
+    const int64_t lim = live ? K : 0;     // a row past the end reads the last one and stores nothing
+    Raw8<XF> xr[VEC];
+    Raw8<RF == FMT_NONE ? FMT_BF16 : RF> rr[VEC];
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
+      const int64_t c = (int64_t)(j * LPR + i) * 8;
+      xr[j] = row_raw8<XF, w()>(static_cast<const char*>(a.X) + rd * a.ldx * xs, c, K);
+      if constexpr (RF != FMT_NONE) rr[j] = row_raw8<RF, w()>(static_cast<const char*>(a.R) + rd * a.ldr * rs, c, K);
+    });
     float h[VEC][8];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      row_load8<XF, WHOLE>(static_cast<const char*>(a.X) + row * a.ldx * xs, (int64_t)(j * LPR + i) * 8, lim, h[j]);
-    if constexpr (RF != FMT_NONE) {
-      float r[VEC][8];
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        row_load8<RF, WHOLE>(static_cast<const char*>(a.R) + row * a.ldr * rs, (int64_t)(j * LPR + i) * 8, lim, r[j]);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) add_residual8<RF, WHOLE>(a, row, (int64_t)(j * LPR + i) * 8, lim, r[j], h[j]);
-    }
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
+      const int64_t c = (int64_t)(j * LPR + i) * 8;
+      row_val8<XF, w()>(xr[j], c, K, h[j]);
+      if constexpr (RF != FMT_NONE) {
+        float r[8];
+        row_val8<RF, w()>(rr[j], c, K, r);
+        add_residual8<RF, w()>(a, row, c, lim, r, h[j]);
+      }
+    });
     float ss = 0.f;
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
@@ -125,13 +140,12 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
     const float s = 1.f / sqrtf(ss / (float)a.K + a.eps);
     if (a.rstd && live && i == 0) a.rstd[row] = s;
     if (!a.Y && !a.q.codes) continue;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = (h[j][e] * s) * gam[j][e];
-      norm_out8<WHOLE>(a, row, (int64_t)(j * LPR + i) * 8, lim, y);
-    }
+      norm_out8<w()>(a, row, (int64_t)(j * LPR + i) * 8, lim, y);
+    });
   }
 }
 
@@ -178,7 +192,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
 // Backward
 // ------------------------------------------------------------------------
 constexpr int NB_T = 1024;                // threads of the backward kernel
-constexpr int NB_MAX_PARTS = 512;         // two workgroups per CU
+constexpr int NB_MAX_PARTS = 512;         // two workgroups per CU, where each has at least four rows per row group
 constexpr int NB_LONG_PARTS = 256;        // of k_rmsnorm_backward_long
 
 // dx of 8 columns: s (g - n mean) + dr.
@@ -190,7 +204,7 @@ __device__ __forceinline__ void norm_dx8(const NormBwdArgs& a, int64_t row, int6
   for (int e = 0; e < 8; ++e) dx[e] = s * fmaf(-n[e], mean, d[e] * g[e]);
   if (a.dR) {
     float r[8];
-    load8_as<WHOLE>(a.dx_fmt, a.dR, row * a.lddr, c, lim, r);
+    load8_as<WHOLE>(a.dx_fmt, a.dR, min(row, a.rows - 1) * a.lddr, c, a.K, r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dx[e] += r[e];
   }
@@ -207,38 +221,57 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
   const int64_t K = a.K;
   const float fk = (float)a.K;
   float gam[VEC][8], dg[VEC][8];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    load8_as<WHOLE>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
+  each_vector<WHOLE, VEC>([&](auto w, int j) {
+    load8_as<w()>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[j][e] = 0.f;
-  }
-  int buf = 0;
-  for (int64_t base = (int64_t)blockIdx.x * RPB; base < a.rows; base += (int64_t)gridDim.x * RPB, buf ^= 1) {
-    const int64_t row = base + threadIdx.x / LPR;
-    const bool live = row < a.rows;
-    const int64_t lim = live ? K : 0;
-    const float s = live ? a.rstd[row] : 0.f;
-    float n[VEC][8], d[VEC][8];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
+  });
+  // With one vector a lane the next row is requested (as stored) before the current
+  // one is reduced, so that its latency passes behind the reduction's barrier; with
+  // two there are no registers for that at 1024 threads.
+  constexpr bool AHEAD = VEC == 1;
+  Raw8<HF> hn[VEC];
+  Raw8<DF> dn[VEC];
+  float sn = 0.f;
+  const auto request = [&](int64_t row) {
+    const int64_t rd = min(row, a.rows - 1);       // past the end: the last row again, cleared below
+    sn = a.rstd[rd];
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
       const int64_t c = (int64_t)(j * LPR + i) * 8;
-      row_load8<HF, WHOLE>(static_cast<const char*>(a.H) + row * a.ldh * hs, c, lim, n[j]);
-      row_load8<DF, WHOLE>(static_cast<const char*>(a.dY) + row * a.lddy * ds, c, lim, d[j]);
-    }
+      hn[j] = row_raw8<HF, w()>(static_cast<const char*>(a.H) + rd * a.ldh * hs, c, K);
+      dn[j] = row_raw8<DF, w()>(static_cast<const char*>(a.dY) + rd * a.lddy * ds, c, K);
+    });
+  };
+  int buf = 0;
+  int64_t base = (int64_t)blockIdx.x * RPB;
+  if (AHEAD) request(base + threadIdx.x / LPR);
+  for (; base < a.rows; base += (int64_t)gridDim.x * RPB, buf ^= 1) {
+    const int64_t row = base + threadIdx.x / LPR;
+    if (!AHEAD) request(row);
+    const bool live = row < a.rows;
+    const float s = sn;
+    float n[VEC][8], d[VEC][8];
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
+      const int64_t c = (int64_t)(j * LPR + i) * 8;
+      row_val8<HF, w()>(hn[j], c, K, n[j]);
+      row_val8<DF, w()>(dn[j], c, K, d[j]);
+    });
+    if (AHEAD) request(row + (int64_t)gridDim.x * RPB);
     float dot = 0.f;
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         n[j][e] *= s;
-        dot = fmaf(d[j][e] * gam[j][e], n[j][e], dot);
-        dg[j][e] = fmaf(d[j][e], n[j][e], dg[j][e]);
+        const float dn = d[j][e] * n[j][e];
+        dot = fmaf(dn, gam[j][e], dot);
+        dg[j][e] += live ? dn : 0.f;
       }
     if (!a.dX) continue;
     const float mean = row_sum<LPR>(dot, part[buf]) / fk;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) norm_dx8<WHOLE>(a, row, (int64_t)(j * LPR + i) * 8, lim, s, mean, n[j], d[j], gam[j]);
+    each_vector<WHOLE, VEC>([&](auto w, int j) {
+      norm_dx8<w()>(a, row, (int64_t)(j * LPR + i) * 8, live ? K : 0, s, mean, n[j], d[j], gam[j]);
+    });
   }
   if (!a.dgamma) return;
   // The workgroup's row groups in order: those of one wave by lane exchange,
@@ -274,11 +307,9 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
       for (int e = 0; e < 8; ++e) dg[j][e] = comb[(j * LPR + i) * 8 + e];
   }
   const int64_t pitch = (K + 3) & ~3ll;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const int64_t c = (int64_t)(j * LPR + i) * 8;
-    row_store8<FMT_F32>(a.ws + blockIdx.x * pitch, c, K, dg[j]);
-  }
+  each_vector<WHOLE, VEC>([&](auto w, int j) {
+    row_store8<FMT_F32, w()>(a.ws + blockIdx.x * pitch, (int64_t)(j * LPR + i) * 8, K, dg[j]);
+  });
 }
 
 // Rows of any length: one row per workgroup, read twice; a workgroup's sums for
@@ -385,8 +416,10 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
 static int norm_bwd_lpr(int64_t K) { return K <= 128 ? 16 : K <= 1024 ? 64 : K <= 4096 ? 256 : 1024; }
 
 int norm_parts(int64_t rows, int64_t K) {
-  const int64_t rpb = NB_T / norm_bwd_lpr(K), most = K > NORM_REG_COLS ? NB_LONG_PARTS : NB_MAX_PARTS;
-  return (int)std::min<int64_t>((rows + rpb - 1) / rpb, most);
+  if (K > NORM_REG_COLS) return (int)std::min<int64_t>(rows, NB_LONG_PARTS);
+  const int64_t rpb = NB_T / norm_bwd_lpr(K), groups = (rows + rpb - 1) / rpb;
+  // a part costs 8 bytes per column: beyond one per CU only where it has four rows to itself
+  return (int)std::min<int64_t>(groups, std::max<int64_t>(256, std::min<int64_t>(groups / 4, NB_MAX_PARTS)));
 }
 
 template <int HF, int DF>

@@ -26,32 +26,29 @@ struct MainAct8 {
   static constexpr int TK = MainBF16::TK;
   static constexpr int OPB = MainBF16::OPB;
   static constexpr int STAGE = MainBF16::STAGE;
-  u32x4 ra[4];
+  Raw8<FMT_BF16> ra[4];
   u32x2 rc[4];
   uint32_t rs[4];
+  int64_t cy, cx, N, K;
+  int tok0, BT;
   bool e4m3;
 
   __device__ __forceinline__ void load(const KArgs8& a, int kc, int row0, int col0) {
     const int tid = threadIdx.x;
     const int f = (tid & 15) * 8;
-    const int64_t cy = row0 + f, cx = col0 + f;
+    cy = row0 + f;
+    cx = col0 + f;
+    N = a.N;
+    K = a.K;
+    BT = a.BT;
+    tok0 = kc * TK + (tid >> 4);
     e4m3 = a.x_fmt == FMT_E4M3;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int tok = kc * TK + (tid >> 4) + 16 * r;
-      const bool in = tok < a.BT;
-      const uint16_t* y = static_cast<const uint16_t*>(a.dY) + (int64_t)tok * a.lddy;
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if (in && cy + 8 <= a.N) {
-        w = *reinterpret_cast<const u32x4_u*>(y + cy);
-      } else if (in) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (cy + i < a.N) w[i >> 1] |= (uint32_t)y[cy + i] << (16 * (i & 1));
-      }
-      ra[r] = w;
-      rc[r] = in ? codes_load8(a.x8.codes + (int64_t)tok * a.x8.ld, cx, a.K) : u32x2{0u, 0u};
-      rs[r] = in && cx < a.K ? (uint32_t)a.x8.scale[(int64_t)tok * a.x8.nb + (cx >> a.x8.sh)] : 0u;
+      const int64_t tok = min(tok0 + 16 * r, a.BT - 1);   // past the end: read again, cleared in store()
+      ra[r] = row_raw8<FMT_BF16>(static_cast<const uint16_t*>(a.dY) + tok * a.lddy, cy, a.N);
+      rc[r] = codes_raw8(a.x8.codes + tok * a.x8.ld, cx, a.K);
+      rs[r] = (uint32_t)a.x8.scale[tok * a.x8.nb + (min(cx, (int64_t)a.K - 1) >> a.x8.sh)];
     }
   }
 
@@ -61,10 +58,15 @@ struct MainAct8 {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int t = (tid >> 4) + 16 * r;
-      const float s = act8_mul(rs[r]);
-      *reinterpret_cast<u32x4*>(stage + MainBF16::off(t, f)) = ra[r];
+      const bool in = tok0 + 16 * r < BT;
+      float y[8];
+      row_val8<FMT_BF16>(ra[r], in ? cy : N, N, y);
+      const u32x4 w = {bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7])};
+      const u32x2 c = codes_val8(rc[r], in ? cx : K, K);
+      const float s = act8_mul(in ? rs[r] : 0u);   // (a cleared code times a NaN scale would be a NaN)
+      *reinterpret_cast<u32x4*>(stage + MainBF16::off(t, f)) = w;
       *reinterpret_cast<u32x4*>(stage + OPB + MainBF16::off(t, f)) =
-          e4m3 ? act8_bf16x8<FMT_E4M3>(rc[r], s) : act8_bf16x8<FMT_S8>(rc[r], s);
+          e4m3 ? act8_bf16x8<FMT_E4M3>(c, s) : act8_bf16x8<FMT_S8>(c, s);
     }
   }
 
@@ -514,14 +516,14 @@ __global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_wide(const KArgs8 a) {
   }
 }
 
-// Any shape.
-template <int OPT, int WF, int MF, int VF>
+// Any shape.  ANY: rows of at least 4 elements (the epilogue's vectors at any alignment).
+template <int OPT, int WF, int MF, int VF, bool ANY>
 __global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
   int ti, tj;
   tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
   const int row0 = ti * TILE, col0 = tj * TILE;
-  Epilogue<Step<OPT, WF, MF, VF, false>, FMT_NONE, false, 4> epi;
+  Epilogue<Step<OPT, WF, MF, VF, false, 0, ANY>, FMT_NONE, false, 4> epi;
   epi.tid = threadIdx.x;
   tile_gradient_by<MainAct8>(a, lds, row0, col0);
   epi.prefetch(a, row0, col0);
@@ -564,8 +566,11 @@ hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st) {
   if (a.x_dma && a.vec_state && a.K % 4 == 0)
     return a.x_fmt == FMT_S8 ? fused_act8_dma<FMT_S8, O, M, V>(a, w_fmt, st)
                              : fused_act8_dma<FMT_E4M3, O, M, V>(a, w_fmt, st);
-  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_fused_act8<O, FMT_BF16, M, V>), tile_grid(a), dim3(NT), 0, st, a);
-  else hipLaunchKernelGGL((k_fused_act8<O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a);
+#define FORGE_ACT8(WF)                                                                                          \
+  if (a.K >= 4) hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, true>), tile_grid(a), dim3(NT), 0, st, a);        \
+  else hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, false>), tile_grid(a), dim3(NT), 0, st, a);
+  if (w_fmt == FMT_BF16) { FORGE_ACT8(FMT_BF16) } else { FORGE_ACT8(FMT_F32) }
+#undef FORGE_ACT8
   return hipGetLastError();
 }
 #define FORGE_INSTANTIATE_ACT8(O, M, V) \
