@@ -81,20 +81,23 @@ __device__ __forceinline__ void act8_decode4(uint32_t w, float f, float* x) {
 // Loads and their decoding are apart, and neither has a branch that depends on the
 // lane (but the skipped load of WHOLE): a load whose value is used inside such a
 // branch is waited for there, one after another, where several should be in flight.
-//  WHOLE: K % 8 == 0, so 8 columns are inside or outside together; outside is 0.
-//  otherwise: the load is of the 8 elements at min(c, K - 8); row_val8 shifts those
-//    of the vector that K ends in into place and clears columns from K on.  (Rows
-//    shorter than 8 are read element by element: the same for all lanes.)
+//  ROW_WHOLE: K % 8 == 0, so 8 columns are inside or outside together; outside is 0.
+//  ROW_BIG: K >= 8; the load is of the 8 elements at min(c, K - 8), row_val8 shifts
+//    those of the vector that K ends in into place and clears columns from K on.
+//  ROW_ANY: ROW_BIG, and rows shorter than 8 element by element (decided at run time,
+//    so each load stands in a branch of its own: for code off the hot path).
+enum RowMode : int { ROW_ANY, ROW_BIG, ROW_WHOLE };
+
 template <int FMT> struct Raw8;
 template <> struct Raw8<FMT_F32> { f32x4 a, b; };
 template <> struct Raw8<FMT_BF16> { u32x4 a; };
 
-template <int FMT, bool WHOLE = false>
+template <int FMT, int MODE = ROW_ANY>
 __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t K) {
   Raw8<FMT> r;
   if constexpr (FMT == FMT_F32) r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
   else r.a = u32x4{0u, 0u, 0u, 0u};
-  if constexpr (WHOLE) {
+  if constexpr (MODE == ROW_WHOLE) {
     if (c < K) {
       if constexpr (FMT == FMT_F32) {
         const float* q = static_cast<const float*>(p) + c;
@@ -104,7 +107,7 @@ __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t 
         r.a = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(p) + c);
       }
     }
-  } else if (K >= 8) {
+  } else if (MODE == ROW_BIG || K >= 8) {
     const int64_t at = min(c, K - 8);
     if constexpr (FMT == FMT_F32) {
       const float* q = static_cast<const float*>(p) + at;
@@ -127,11 +130,11 @@ __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t 
   return r;
 }
 
-template <int FMT, bool WHOLE = false>
+template <int FMT, int MODE = ROW_ANY>
 __device__ __forceinline__ void row_val8(Raw8<FMT> r, int64_t c, int64_t K, float (&x)[8]) {
-  if constexpr (!WHOLE) {
+  if constexpr (MODE != ROW_WHOLE) {
     // elements the load began too early (rows shorter than 8 begin at 0: nothing to shift for c = 0)
-    const int s = K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
+    const int s = MODE == ROW_BIG || K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
     if constexpr (FMT == FMT_F32) {
       const f32x4 z = {0.f, 0.f, 0.f, 0.f};
       r.a = s & 4 ? r.b : r.a;
@@ -164,21 +167,21 @@ __device__ __forceinline__ void row_val8(Raw8<FMT> r, int64_t c, int64_t K, floa
   }
 }
 
-template <int FMT, bool WHOLE = false>
+template <int FMT, int MODE = ROW_ANY>
 __device__ __forceinline__ void row_load8(const void* p, int64_t c, int64_t K, float (&x)[8]) {
-  row_val8<FMT, WHOLE>(row_raw8<FMT, WHOLE>(p, c, K), c, K, x);
+  row_val8<FMT, MODE>(row_raw8<FMT, MODE>(p, c, K), c, K, x);
 }
 
 // The reverse: 8 values rounded to FMT (nearest even); columns from K on are not
 // written (the vector that K ends in: 4, 2 and 1 elements as its length asks).
-template <int FMT, bool WHOLE = false>
+template <int FMT, int MODE = ROW_ANY>
 __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const float (&x)[8]) {
   if constexpr (FMT == FMT_F32) {
     float* q = static_cast<float*>(p) + c;
     if (c + 8 <= K) {
       *reinterpret_cast<f32x4_u*>(q) = f32x4{x[0], x[1], x[2], x[3]};
       *reinterpret_cast<f32x4_u*>(q + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    } else if (!WHOLE && c < K) {
+    } else if (MODE != ROW_WHOLE && c < K) {
       const int n = (int)(K - c);
       float y[4] = {x[0], x[1], x[2], x[3]};
       if (n & 4) {
@@ -199,7 +202,7 @@ __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const 
     const u32x4 w = {bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7])};
     if (c + 8 <= K) {
       *reinterpret_cast<u32x4_u*>(q) = w;
-    } else if (!WHOLE && c < K) {
+    } else if (MODE != ROW_WHOLE && c < K) {
       const int n = (int)(K - c);
       uint32_t y0 = w[0], y1 = w[1];
       if (n & 4) {
@@ -219,12 +222,12 @@ __device__ __forceinline__ void row_store8(void* p, int64_t c, int64_t K, const 
 }
 
 // Store 8 codes of a row; columns from K on are not written.
-template <bool WHOLE = false>
+template <int MODE = ROW_ANY>
 __device__ __forceinline__ void codes_store8(uint8_t* p, int64_t c, int64_t K, u32x2 w) {
   uint8_t* q = p + c;
   if (c + 8 <= K) {
     *reinterpret_cast<u32x2_u*>(q) = w;
-  } else if (!WHOLE && c < K) {
+  } else if (MODE != ROW_WHOLE && c < K) {
     const int n = (int)(K - c);
     uint32_t y = w[0];
     if (n & 4) {
@@ -242,14 +245,16 @@ __device__ __forceinline__ void codes_store8(uint8_t* p, int64_t c, int64_t K, u
   }
 }
 // 8 codes at column c, the same way: the load, then codes_val8.
+template <int MODE = ROW_ANY>
 __device__ __forceinline__ u32x2 codes_raw8(const uint8_t* p, int64_t c, int64_t K) {
-  if (K >= 8) return *reinterpret_cast<const u32x2_u*>(p + min(c, K - 8));
+  if (MODE == ROW_BIG || K >= 8) return *reinterpret_cast<const u32x2_u*>(p + min(c, K - 8));
   u32x2 w = {0u, 0u};
   for (int64_t i = K - 1; i >= 0; --i) w = u32x2{(w[0] << 8) | p[i], (w[1] << 8) | (w[0] >> 24)};
   return w;
 }
+template <int MODE = ROW_ANY>
 __device__ __forceinline__ u32x2 codes_val8(u32x2 w, int64_t c, int64_t K) {
-  const int s = K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
+  const int s = MODE == ROW_BIG || K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
   const uint32_t lo = s & 4 ? w[1] : w[0], hi = s & 4 ? 0u : w[1];
   const u32x2 v = {__builtin_amdgcn_alignbyte(hi, lo, s & 3), hi >> (8 * (s & 3))};
   return s & 8 ? u32x2{0u, 0u} : v;
@@ -258,7 +263,7 @@ __device__ __forceinline__ u32x2 codes_val8(u32x2 w, int64_t c, int64_t K) {
 // Quantise and store the 8 values at column c of row r, the lane's share of a
 // block that spans 2^sh / 8 adjacent lanes (values from K on are 0).  Every lane
 // of a block's group must call this together.
-template <int FMT, bool WHOLE = false>
+template <int FMT, int MODE = ROW_ANY>
 __device__ __forceinline__ void act8_store8(const Act8& q, int64_t r, int64_t c, int64_t K, const float (&x)[8]) {
   uint32_t a = 0;
 #pragma unroll
@@ -267,8 +272,33 @@ __device__ __forceinline__ void act8_store8(const Act8& q, int64_t r, int64_t c,
   const uint32_t byte = act8_scale_byte<FMT>(a);
   const u32x2 w = act8_encode<FMT>(x, act8_inv(byte), byte == ACT8_NAN);
   if (c >= K) return;
-  codes_store8<WHOLE>(q.codes + r * q.ld, c, K, w);
+  codes_store8<MODE>(q.codes + r * q.ld, c, K, w);
   if ((c & ((1 << q.sh) - 1)) == 0) q.scale[r * q.nb + (c >> q.sh)] = (uint8_t)byte;
+}
+
+// s += the rows at(0) .. at(mine - 1) of an array of type FMT at column c, in order.
+// at(i) is the address of a row's element 0, valid for every i (callers clamp it);
+// count: the largest `mine` of the wave.  8 or 4 rows are in flight at a time, those
+// past the lane's own count read and left out, so no load waits for another.
+template <int MODE, int FMT, int B, class AT>
+__device__ __forceinline__ void sum_rows_batch(AT&& at, int m, int mine, int64_t c, int64_t K, float (&s)[8]) {
+  Raw8<FMT> r[B];
+#pragma unroll
+  for (int u = 0; u < B; ++u) r[u] = row_raw8<FMT, MODE>(at(m + u), c, K);
+#pragma unroll
+  for (int u = 0; u < B; ++u) {
+    float x[8];
+    row_val8<FMT, MODE>(r[u], c, K, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = m + u < mine ? s[k] + x[k] : s[k];
+  }
+}
+template <int MODE, int FMT, class AT>
+__device__ __forceinline__ void sum_rows(AT&& at, int count, int mine, int64_t c, int64_t K, float (&s)[8]) {
+  int m = 0;
+  for (; count - m > 4; m += 8) sum_rows_batch<MODE, FMT, 8>(at, m, mine, c, K, s);
+  if (count - m > 1) sum_rows_batch<MODE, FMT, 4>(at, m, mine, c, K, s);
+  else if (count - m == 1) sum_rows_batch<MODE, FMT, 1>(at, m, mine, c, K, s);
 }
 
 }  // namespace forge

@@ -14,18 +14,18 @@ namespace forge {
 // order, then over the slots in a fixed order.  rng: 2 ROWS ints, red: 3 x 128 floats.
 constexpr int LONG_ROW = 32;
 
-template <int DF>
-__device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int n, int step, int64_t c, float (&s)[8]) {
+// Tokens slot, slot + step, .. of first .. last - 1 of the sorted ones, and then the sum
+// over the wave's 4 slots.  (A slot with no token of its own has mine <= 0.)
+template <int MODE, int DF>
+__device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int last, int slot, int step, int64_t c,
+                                              float (&s)[8]) {
   constexpr int ds = DF == FMT_F32 ? 4 : 2;
 #pragma unroll
   for (int k = 0; k < 8; ++k) s[k] = 0.f;
-#pragma unroll 4
-  for (int i = first; i < n; i += step) {
-    float x[8];
-    row_load8<DF>(static_cast<const char*>(e.dY) + (int64_t)e.perm[i] * e.lddy * ds, c, e.K, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] += x[k];
-  }
+  const auto at = [&](int i) {
+    return static_cast<const char*>(e.dY) + (int64_t)e.perm[min(first + slot + i * step, last - 1)] * e.lddy * ds;
+  };
+  sum_rows<MODE, DF>(at, (last - first + step - 1) / step, (last - first - slot + step - 1) / step, c, e.K, s);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     s[k] += __shfl_xor(s[k], 16);
@@ -33,7 +33,7 @@ __device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int
   }
 }
 
-template <int DF, int ROWS>
+template <int MODE, int DF, int ROWS>
 __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* rng, float* red, int row0, int col0, int first,
                                            int last) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -62,7 +62,7 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
       const int k = base + __builtin_ctzll(mine);
       mine &= mine - 1;
       float s[8];
-      gather_tokens<DF>(e, rng[2 * k] + (lane >> 4), rng[2 * k + 1], 4, c, s);
+      gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], lane >> 4, 4, c, s);
       if (lane < 16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) sG[k * GP + cl + i] = s[i] * e.scale;
@@ -72,7 +72,7 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
       const int k = base + __builtin_ctzll(all);
       all &= all - 1;
       float s[8];
-      gather_tokens<DF>(e, rng[2 * k] + (tid >> 4), rng[2 * k + 1], 16, c, s);
+      gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], tid >> 4, 16, c, s);
       if (wave > 0 && lane < 16) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) red[(wave - 1) * TILE + cl + i] = s[i];
@@ -90,20 +90,21 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
   __syncthreads();
 }
 
-// ANY: rows of any alignment, at least 4 elements long.
+// FAST, ANY: rows of at least 8 elements, ANY of any alignment.
 template <int ROWS, bool FAST, bool ANY, int OPT, int WF, int MF, int VF>
 __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const EmbedArgs e) {
   __shared__ __attribute__((aligned(16))) float sG[ROWS * GP];
   __shared__ int rng[2 * ROWS];
   __shared__ float red[3 * TILE];
+  constexpr int MODE = FAST || ANY ? ROW_BIG : ROW_ANY;
   const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
   const int row0 = ti * ROWS, col0 = tj * TILE;
   Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, ROWS> epi;
   epi.tid = threadIdx.x;
   epi.prefetch(a, row0, col0);
   const int first = e.T ? e.tile[ti] : 0, last = e.T ? e.tile[ti + 1] : 0;
-  if (e.dy_fmt == FMT_F32) embed_tile<FMT_F32, ROWS>(e, sG, rng, red, row0, col0, first, last);
-  else embed_tile<FMT_BF16, ROWS>(e, sG, rng, red, row0, col0, first, last);
+  if (e.dy_fmt == FMT_F32) embed_tile<MODE, FMT_F32, ROWS>(e, sG, rng, red, row0, col0, first, last);
+  else embed_tile<MODE, FMT_BF16, ROWS>(e, sG, rng, red, row0, col0, first, last);
   epi.run_prefetched(a, sG, row0, col0);
 }
 
@@ -111,9 +112,9 @@ __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const Embed
 // step is bound by the gathering of each tile's tokens, not by HBM.
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
-  const bool fast = a.vec_state && (a.K % 4) == 0;
+  const bool fast = a.vec_state && a.K % 4 == 0 && a.K >= 8;
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
-  const int64_t rows = (int64_t)a.tiles_n * a.tiles_k >= 512 && a.K >= 4 ? TILE : EMBED_MIN_ROWS;
+  const int64_t rows = (int64_t)a.tiles_n * a.tiles_k >= 512 && a.K >= 8 ? TILE : EMBED_MIN_ROWS;
   const int64_t tiles = (a.N + rows - 1) / rows;
   if (e.T > 0) {
     const hipError_t err = launch_embed_tiles(e, rows, tiles, st);
@@ -129,7 +130,7 @@ hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_
     FORGE_EMBED(TILE, false, true)
   }
   if (fast) { FORGE_EMBED(EMBED_MIN_ROWS, true, false) }
-  if (a.K >= 4) { FORGE_EMBED(EMBED_MIN_ROWS, false, true) }
+  if (a.K >= 8) { FORGE_EMBED(EMBED_MIN_ROWS, false, true) }
   FORGE_EMBED(EMBED_MIN_ROWS, false, false)
 #undef FORGE_EMBED
 }

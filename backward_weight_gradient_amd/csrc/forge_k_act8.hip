@@ -25,7 +25,7 @@ struct ActArgs {
   int64_t units;    // (rows / (rows per workgroup), segment) pairs
 };
 
-template <int XF, int QF>
+template <int MODE, int XF, int QF>
 __device__ __forceinline__ void quantize_unit(const ActArgs& a, int64_t unit) {
   const int64_t rb = unit / a.segs;
   const int seg = (int)(unit - rb * a.segs);
@@ -37,18 +37,18 @@ __device__ __forceinline__ void quantize_unit(const ActArgs& a, int64_t unit) {
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = min(r0 + (int64_t)u * rpb, a.rows - 1);   // a row past the end: read again, not stored
-    w[u] = row_raw8<XF>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K);
+    w[u] = row_raw8<XF, MODE>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K);
   }
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = r0 + (int64_t)u * rpb;
     float x[8];
-    row_val8<XF>(w[u], c, a.K, x);
+    row_val8<XF, MODE>(w[u], c, a.K, x);
     act8_store8<QF>(a.q, r, r < a.rows ? c : a.K, a.K, x);
   }
 }
 
-template <int XF, int QF>
+template <int MODE, int XF, int QF>
 __device__ __forceinline__ void dequantize_unit(const ActArgs& a, int64_t unit) {
   const int64_t rb = unit / a.segs;
   const int seg = (int)(unit - rb * a.segs);
@@ -62,7 +62,7 @@ __device__ __forceinline__ void dequantize_unit(const ActArgs& a, int64_t unit) 
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = min(r0 + (int64_t)u * rpb, a.rows - 1);
-    w[u] = codes_raw8(a.q.codes + r * a.q.ld, c, a.K);
+    w[u] = codes_raw8<MODE>(a.q.codes + r * a.q.ld, c, a.K);
     s[u] = a.q.scale[r * a.q.nb + (c >> a.q.sh)];
   }
 #pragma unroll
@@ -71,18 +71,18 @@ __device__ __forceinline__ void dequantize_unit(const ActArgs& a, int64_t unit) 
     if (r >= a.rows) return;
     float x[8];
     const float f = act8_mul(s[u]);
-    const u32x2 v = codes_val8(w[u], c, a.K);
+    const u32x2 v = codes_val8<MODE>(w[u], c, a.K);
     act8_decode4<QF>(v[0], f, x);
     act8_decode4<QF>(v[1], f, x + 4);
     row_store8<XF>(static_cast<char*>(a.Xo) + r * a.ldx * es, c, a.K, x);
   }
 }
 
-template <bool QUANT, int XF, int QF>
+template <bool QUANT, int MODE, int XF, int QF>
 __global__ void __launch_bounds__(NT) k_act(const ActArgs a) {
   for (int64_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-    if constexpr (QUANT) quantize_unit<XF, QF>(a, unit);
-    else dequantize_unit<XF, QF>(a, unit);
+    if constexpr (QUANT) quantize_unit<MODE, XF, QF>(a, unit);
+    else dequantize_unit<MODE, XF, QF>(a, unit);
   }
 }
 
@@ -109,7 +109,8 @@ static hipError_t launch_act(ActArgs a, int x_fmt, int q_fmt, hipStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>(a.units, 1 << 22);
 #define FORGE_ACT(XF, QF)                                                                                     \
   if (x_fmt == XF && q_fmt == QF) {                                                      \
-    hipLaunchKernelGGL((k_act<QUANT, XF, QF>), dim3(grid), dim3(NT), 0, st, a);          \
+    if (a.K >= 8) hipLaunchKernelGGL((k_act<QUANT, ROW_BIG, XF, QF>), dim3(grid), dim3(NT), 0, st, a); \
+    else hipLaunchKernelGGL((k_act<QUANT, ROW_ANY, XF, QF>), dim3(grid), dim3(NT), 0, st, a);          \
     return hipGetLastError();                                                            \
   }
   FORGE_ACT(FMT_BF16, FMT_S8)

@@ -20,6 +20,16 @@ __device__ __forceinline__ void load_ids(const void* ids, int id_bytes, F&& at, 
   }
 }
 
+// Zero a matrix of format fmt.
+__global__ void __launch_bounds__(NT) k_zero_rows(void* p, int64_t ld, int fmt, int64_t rows, int64_t K) {
+  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < K; c += NT * 8) {
+      if (fmt == FMT_F32) row_store8<FMT_F32>(static_cast<float*>(p) + r * ld, c, K, z);
+      else row_store8<FMT_BF16>(static_cast<uint16_t*>(p) + r * ld, c, K, z);
+    }
+}
+
 // ------------------------------------------------------------------------
 // Lookup: Y[t] = scale W[ids[t]].  A gather of whole rows: s bytes read and
 // written per element, bound by HBM.  Threads map to (token, 8 columns) as in
@@ -38,7 +48,7 @@ struct LookupArgs {
   int64_t units;
 };
 
-template <int WF, int YF>
+template <int MODE, int WF, int YF>
 __global__ void __launch_bounds__(NT) k_embed(const LookupArgs a) {
   const int tpr = 1 << a.tsh, rpb = NT >> a.tsh;
   constexpr int ws = WF == FMT_F32 ? 4 : 2, ys = YF == FMT_F32 ? 4 : 2;
@@ -54,14 +64,14 @@ __global__ void __launch_bounds__(NT) k_embed(const LookupArgs a) {
 #pragma unroll
     for (int u = 0; u < EMB_UNR; ++u) {
       row[u] = id_row(row[u], a.V);
-      // (padding reads row 0 and is cleared; V may be 0)
-      w[u] = row_raw8<WF>(static_cast<const char*>(a.W) + (row[u] < a.V ? row[u] : 0) * a.ldw * ws, c, a.V > 0 ? a.K : 0);
+      // (padding reads row 0 and is cleared)
+      w[u] = row_raw8<WF, MODE>(static_cast<const char*>(a.W) + (row[u] < a.V ? row[u] : 0) * a.ldw * ws, c, a.K);
     }
 #pragma unroll
     for (int u = 0; u < EMB_UNR; ++u) {
       const int64_t t = t0 + (int64_t)u * rpb;
       float x[8];
-      row_val8<WF>(w[u], c, a.V > 0 ? a.K : 0, x);
+      row_val8<WF, MODE>(w[u], c, a.K, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = row[u] < a.V ? x[e] * a.scale : 0.f;
       if (t < a.T) row_store8<YF>(static_cast<char*>(a.Y) + t * a.ldy * ys, c, a.K, x);
@@ -72,6 +82,10 @@ __global__ void __launch_bounds__(NT) k_embed(const LookupArgs a) {
 hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
                         int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t st) {
   if (T == 0 || K == 0) return hipSuccess;
+  if (V == 0) {   // nothing but padding
+    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)std::min<int64_t>(T, 1 << 20)), dim3(NT), 0, st, Y, ldy, y_fmt, T, K);
+    return hipGetLastError();
+  }
   LookupArgs a{ids, id_bytes, T, V, K, W, ldw, Y, ldy, scale, 0, 0, 0};
   const int64_t lanes = (K + 7) / 8;
   a.tsh = 0;
@@ -81,11 +95,15 @@ hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W,
   a.units = ((T + rpb - 1) / rpb) * a.segs;
   const dim3 grid((unsigned)std::min<int64_t>(a.units, 1 << 22)), b(NT);
   const bool wf = w_fmt == FMT_F32, yf = y_fmt == FMT_F32;
-  if (wf && yf) hipLaunchKernelGGL((k_embed<FMT_F32, FMT_F32>), grid, b, 0, st, a);
-  else if (wf) hipLaunchKernelGGL((k_embed<FMT_F32, FMT_BF16>), grid, b, 0, st, a);
-  else if (yf) hipLaunchKernelGGL((k_embed<FMT_BF16, FMT_F32>), grid, b, 0, st, a);
-  else hipLaunchKernelGGL((k_embed<FMT_BF16, FMT_BF16>), grid, b, 0, st, a);
+#define FORGE_LOOKUP(MODE)                                                                        \
+  if (wf && yf) hipLaunchKernelGGL((k_embed<MODE, FMT_F32, FMT_F32>), grid, b, 0, st, a);         \
+  else if (wf) hipLaunchKernelGGL((k_embed<MODE, FMT_F32, FMT_BF16>), grid, b, 0, st, a);         \
+  else if (yf) hipLaunchKernelGGL((k_embed<MODE, FMT_BF16, FMT_F32>), grid, b, 0, st, a);         \
+  else hipLaunchKernelGGL((k_embed<MODE, FMT_BF16, FMT_BF16>), grid, b, 0, st, a);                \
   return hipGetLastError();
+  if (K >= 8) { FORGE_LOOKUP(ROW_BIG) }
+  FORGE_LOOKUP(ROW_ANY)
+#undef FORGE_LOOKUP
 }
 
 // ------------------------------------------------------------------------
@@ -226,7 +244,7 @@ __device__ __forceinline__ int64_t run_end(const EmbedArgs& e, int64_t p, int v,
 
 constexpr int ROW_PERM = 1024;          // tokens of a long row staged in LDS at a time
 
-template <int DF>
+template <int MODE, int DF>
 __device__ __forceinline__ void rows_long(const EmbedArgs& e, float* acc, int64_t ldacc, int add, int64_t unit, int64_t segs,
                                           float (&sum)[4][ROW_SEG], int32_t (&tok)[ROW_PERM]) {
   constexpr int ds = DF == FMT_F32 ? 4 : 2;
@@ -246,13 +264,10 @@ __device__ __forceinline__ void rows_long(const EmbedArgs& e, float* acc, int64_
     __syncthreads();                                                // the tokens staged before are read
     for (int i = threadIdx.x; i < n; i += NT) tok[i] = e.perm[b + i];
     __syncthreads();
-#pragma unroll 8
-    for (int i = slot; i < n; i += 32) {
-      float x[8];
-      row_load8<DF>(static_cast<const char*>(e.dY) + (int64_t)tok[i] * e.lddy * ds, c, e.K, x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += x[k];
-    }
+    const auto at = [&](int i) {
+      return static_cast<const char*>(e.dY) + (int64_t)tok[min(slot + 32 * i, n - 1)] * e.lddy * ds;
+    };
+    sum_rows<MODE, DF>(at, (n + 31) / 32, (n - slot + 31) / 32, c, e.K, s);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -273,7 +288,7 @@ __device__ __forceinline__ void rows_long(const EmbedArgs& e, float* acc, int64_
   }
 }
 
-template <int DF>
+template <int MODE, int DF>
 __device__ __forceinline__ void rows_short(const EmbedArgs& e, float* acc, int64_t ldacc, int add, int64_t p, int64_t c0) {
   constexpr int ds = DF == FMT_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
@@ -286,54 +301,43 @@ __device__ __forceinline__ void rows_short(const EmbedArgs& e, float* acc, int64
   const int64_t c = c0 + 8 * lane;
   float* o = acc + (int64_t)v * ldacc;
   Raw8<FMT_F32> old;
-  if (add) old = row_raw8<FMT_F32>(o, c, e.K);
+  if (add) old = row_raw8<FMT_F32, MODE>(o, c, e.K);
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    float x[8];
-    const int64_t t = __builtin_amdgcn_readlane(tok, i);
-    row_load8<DF>(static_cast<const char*>(e.dY) + t * e.lddy * ds, c, e.K, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] += x[k];
-  }
+  const auto at = [&](int i) {
+    return static_cast<const char*>(e.dY) + (int64_t)__builtin_amdgcn_readlane(tok, min(i, n - 1)) * e.lddy * ds;
+  };
+  sum_rows<MODE, DF>(at, n, n, c, e.K, s);
 #pragma unroll
   for (int k = 0; k < 8; ++k) s[k] *= e.scale;
   if (add) {
     float x[8];
-    row_val8<FMT_F32>(old, c, e.K, x);
+    row_val8<FMT_F32, MODE>(old, c, e.K, x);
 #pragma unroll
     for (int k = 0; k < 8; ++k) s[k] = x[k] + s[k];
   }
   row_store8<FMT_F32>(o, c, e.K, s);
 }
 
-template <int DF>
+template <int MODE, int DF>
 __global__ void __launch_bounds__(NT) k_embed_rows(const EmbedArgs e, float* acc, int64_t ldacc, int add, int longs) {
   __shared__ float sum[4][ROW_SEG];
   __shared__ int32_t tok[ROW_PERM];
   if ((int)blockIdx.x < longs) {
     const int64_t segs = (e.K + ROW_SEG - 1) / ROW_SEG, units = (e.T + ROW_LONG - 1) / ROW_LONG * segs;
-    for (int64_t u = blockIdx.x; u < units; u += longs) rows_long<DF>(e, acc, ldacc, add, u, segs, sum, tok);
+    for (int64_t u = blockIdx.x; u < units; u += longs) rows_long<MODE, DF>(e, acc, ldacc, add, u, segs, sum, tok);
   } else {
     const int64_t groups = (e.K + ROW_COLS - 1) / ROW_COLS;
     const int64_t stride = (int64_t)(gridDim.x - longs) * 4;
     for (int64_t u = ((int64_t)blockIdx.x - longs) * 4 + (threadIdx.x >> 6); u < e.T * groups; u += stride)
-      rows_short<DF>(e, acc, ldacc, add, u / groups, u % groups * ROW_COLS);
+      rows_short<MODE, DF>(e, acc, ldacc, add, u / groups, u % groups * ROW_COLS);
   }
-}
-
-// Zero rows of an fp32 matrix.
-__global__ void __launch_bounds__(NT) k_embed_zero(float* acc, int64_t ld, int64_t V, int64_t K) {
-  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int64_t v = blockIdx.x; v < V; v += gridDim.x)
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < K; c += NT * 8) row_store8<FMT_F32>(acc + v * ld, c, K, z);
 }
 
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t st) {
   if (e.V == 0 || e.K == 0) return hipSuccess;
   if (first) {
-    hipLaunchKernelGGL(k_embed_zero, dim3((unsigned)std::min<int64_t>(e.V, 1 << 20)), dim3(NT), 0, st, acc, ldacc, e.V,
-                       e.K);
+    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)std::min<int64_t>(e.V, 1 << 20)), dim3(NT), 0, st, acc, ldacc,
+                       (int)FMT_F32, e.V, e.K);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -344,11 +348,14 @@ hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc
   const int64_t shorts = (e.T * ((e.K + ROW_COLS - 1) / ROW_COLS) + 3) / 4;
   const int longs = (int)std::min<int64_t>(long_units, 2048);
   const dim3 grid((unsigned)(longs + std::min<int64_t>(shorts, 1 << 20)));
-  if (e.dy_fmt == FMT_F32)
-    hipLaunchKernelGGL((k_embed_rows<FMT_F32>), grid, dim3(NT), 0, st, e, acc, ldacc, first ? 0 : 1, longs);
-  else
-    hipLaunchKernelGGL((k_embed_rows<FMT_BF16>), grid, dim3(NT), 0, st, e, acc, ldacc, first ? 0 : 1, longs);
+#define FORGE_ROWS(MODE)                                                                                                        \
+  if (e.dy_fmt == FMT_F32)                                                                                                      \
+    hipLaunchKernelGGL((k_embed_rows<MODE, FMT_F32>), grid, dim3(NT), 0, st, e, acc, ldacc, first ? 0 : 1, longs);              \
+  else hipLaunchKernelGGL((k_embed_rows<MODE, FMT_BF16>), grid, dim3(NT), 0, st, e, acc, ldacc, first ? 0 : 1, longs);          \
   return hipGetLastError();
+  if (e.K >= 8) { FORGE_ROWS(ROW_BIG) }
+  FORGE_ROWS(ROW_ANY)
+#undef FORGE_ROWS
 }
 
 // tile[i] = the first place whose row is >= i * rows, for i = 0 .. tiles (the step's

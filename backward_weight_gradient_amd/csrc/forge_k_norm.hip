@@ -45,34 +45,34 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
   return x;
 }
 
-template <bool WHOLE>
+template <int MODE>
 __device__ __forceinline__ void load8_as(int fmt, const void* base, int64_t elem, int64_t c, int64_t K, float (&x)[8]) {
-  if (fmt == FMT_F32) row_load8<FMT_F32, WHOLE>(static_cast<const float*>(base) + elem, c, K, x);
-  else row_load8<FMT_BF16, WHOLE>(static_cast<const uint16_t*>(base) + elem, c, K, x);
+  if (fmt == FMT_F32) row_load8<FMT_F32, MODE>(static_cast<const float*>(base) + elem, c, K, x);
+  else row_load8<FMT_BF16, MODE>(static_cast<const uint16_t*>(base) + elem, c, K, x);
 }
-template <bool WHOLE>
+template <int MODE>
 __device__ __forceinline__ void store8_as(int fmt, void* base, int64_t elem, int64_t c, int64_t K, const float (&x)[8]) {
-  if (fmt == FMT_F32) row_store8<FMT_F32, WHOLE>(static_cast<float*>(base) + elem, c, K, x);
-  else row_store8<FMT_BF16, WHOLE>(static_cast<uint16_t*>(base) + elem, c, K, x);
+  if (fmt == FMT_F32) row_store8<FMT_F32, MODE>(static_cast<float*>(base) + elem, c, K, x);
+  else row_store8<FMT_BF16, MODE>(static_cast<uint16_t*>(base) + elem, c, K, x);
 }
 
 constexpr int norm_threads(int lpr) { return lpr > 256 ? lpr : 256; }
 
 // 8 columns of a row: Y and the 8-bit copy.
-template <bool WHOLE>
+template <int MODE>
 __device__ __forceinline__ void norm_out8(const NormArgs& a, int64_t row, int64_t c, int64_t lim, const float (&y)[8]) {
-  if (a.Y) store8_as<WHOLE>(a.y_fmt, a.Y, row * a.ldy, c, lim, y);
+  if (a.Y) store8_as<MODE>(a.y_fmt, a.Y, row * a.ldy, c, lim, y);
   if (a.q.codes) {
     float z[8];       // columns from K on do not count in a block's absmax (0 * s may be NaN)
 #pragma unroll
     for (int e = 0; e < 8; ++e) z[e] = c + e < lim ? y[e] : 0.f;
-    if (a.q_fmt == FMT_S8) act8_store8<FMT_S8, WHOLE>(a.q, row, c, lim, z);
-    else act8_store8<FMT_E4M3, WHOLE>(a.q, row, c, lim, z);
+    if (a.q_fmt == FMT_S8) act8_store8<FMT_S8, MODE>(a.q, row, c, lim, z);
+    else act8_store8<FMT_E4M3, MODE>(a.q, row, c, lim, z);
   }
 }
 
 // h = x + r, rounded to r's type and stored as H.
-template <int RF, bool WHOLE>
+template <int RF, int MODE>
 __device__ __forceinline__ void add_residual8(const NormArgs& a, int64_t row, int64_t c, int64_t lim, const float (&r)[8],
                                               float (&h)[8]) {
 #pragma unroll
@@ -85,20 +85,19 @@ __device__ __forceinline__ void add_residual8(const NormArgs& a, int64_t row, in
       h[e + 1] = __uint_as_float(w & 0xFFFF0000u);
     }
   }
-  row_store8<RF, WHOLE>(static_cast<char*>(a.H) + row * a.ldh * (RF == FMT_F32 ? 4 : 2), c, lim, h);
+  row_store8<RF, MODE>(static_cast<char*>(a.H) + row * a.ldh * (RF == FMT_F32 ? 4 : 2), c, lim, h);
 }
 
-// A row that needs VEC vectors ends in the last of them: f<whole>(j) with whole = true
-// for the others.
-template <bool WHOLE, int VEC, class F>
+// A row that needs VEC vectors ends in the last of them; the others are whole.
+template <int MODE, int VEC, class F>
 __device__ __forceinline__ void each_vector(F&& f) {
 #pragma unroll
-  for (int j = 0; j + 1 < VEC; ++j) f(std::true_type{}, j);
-  f(std::integral_constant<bool, WHOLE>{}, VEC - 1);
+  for (int j = 0; j + 1 < VEC; ++j) f(std::integral_constant<int, ROW_WHOLE>{}, j);
+  f(std::integral_constant<int, MODE>{}, VEC - 1);
 }
 
 // RF: the residual's format, FMT_NONE without one.
-template <int XF, int RF, int LPR, int VEC, bool WHOLE>
+template <int XF, int RF, int LPR, int VEC, int MODE>
 __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a) {
   constexpr int THREADS = norm_threads(LPR), RPB = THREADS / LPR;
   constexpr int xs = XF == FMT_F32 ? 4 : 2, rs = RF == FMT_F32 ? 4 : 2;
@@ -106,7 +105,7 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
   const int i = threadIdx.x & (LPR - 1);
   const int64_t K = a.K;
   float gam[VEC][8];
-  each_vector<WHOLE, VEC>([&](auto w, int j) {
+  each_vector<MODE, VEC>([&](auto w, int j) {
     load8_as<w()>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
   });
   int buf = 0;
@@ -116,13 +115,13 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
     const int64_t lim = live ? K : 0;     // a row past the end reads the last one and stores nothing
     Raw8<XF> xr[VEC];
     Raw8<RF == FMT_NONE ? FMT_BF16 : RF> rr[VEC];
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       const int64_t c = (int64_t)(j * LPR + i) * 8;
       xr[j] = row_raw8<XF, w()>(static_cast<const char*>(a.X) + rd * a.ldx * xs, c, K);
       if constexpr (RF != FMT_NONE) rr[j] = row_raw8<RF, w()>(static_cast<const char*>(a.R) + rd * a.ldr * rs, c, K);
     });
     float h[VEC][8];
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       const int64_t c = (int64_t)(j * LPR + i) * 8;
       row_val8<XF, w()>(xr[j], c, K, h[j]);
       if constexpr (RF != FMT_NONE) {
@@ -140,7 +139,7 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
     const float s = 1.f / sqrtf(ss / (float)a.K + a.eps);
     if (a.rstd && live && i == 0) a.rstd[row] = s;
     if (!a.Y && !a.q.codes) continue;
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = (h[j][e] * s) * gam[j][e];
@@ -149,7 +148,7 @@ __global__ void __launch_bounds__(norm_threads(LPR)) k_rmsnorm(const NormArgs a)
   }
 }
 
-// Rows of any length: one row per 1024-thread workgroup, read a second time (H,
+// Rows of any length: one per 1024-thread workgroup, read a second time (H,
 // or X without a residual) for the output.
 template <int XF, int RF>
 __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
       if constexpr (RF != FMT_NONE) {
         float r[8];
         row_load8<RF>(static_cast<const char*>(a.R) + row * a.ldr * rs, c, K, r);
-        add_residual8<RF, false>(a, row, c, K, r, h);
+        add_residual8<RF, ROW_ANY>(a, row, c, K, r, h);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(h[e], h[e], ss);
@@ -180,10 +179,10 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
       // (what this thread itself stored as H above)
       if constexpr (RF != FMT_NONE) row_load8<RF>(static_cast<const char*>(a.H) + row * a.ldh * rs, c, K, h);
       else row_load8<XF>(static_cast<const char*>(a.X) + row * a.ldx * xs, c, K, h);
-      load8_as<false>(a.g_fmt, a.gamma, 0, c, K, g);
+      load8_as<ROW_ANY>(a.g_fmt, a.gamma, 0, c, K, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = (h[e] * s) * g[e];
-      norm_out8<false>(a, row, c, K, y);
+      norm_out8<ROW_ANY>(a, row, c, K, y);
     }
   }
 }
@@ -196,7 +195,7 @@ constexpr int NB_MAX_PARTS = 512;         // two workgroups per CU, where each h
 constexpr int NB_LONG_PARTS = 256;        // of k_rmsnorm_backward_long
 
 // dx of 8 columns: s (g - n mean) + dr.
-template <bool WHOLE>
+template <int MODE>
 __device__ __forceinline__ void norm_dx8(const NormBwdArgs& a, int64_t row, int64_t c, int64_t lim, float s, float mean,
                                          const float (&n)[8], const float (&d)[8], const float (&g)[8]) {
   float dx[8];
@@ -204,14 +203,14 @@ __device__ __forceinline__ void norm_dx8(const NormBwdArgs& a, int64_t row, int6
   for (int e = 0; e < 8; ++e) dx[e] = s * fmaf(-n[e], mean, d[e] * g[e]);
   if (a.dR) {
     float r[8];
-    load8_as<WHOLE>(a.dx_fmt, a.dR, min(row, a.rows - 1) * a.lddr, c, a.K, r);
+    load8_as<MODE>(a.dx_fmt, a.dR, min(row, a.rows - 1) * a.lddr, c, a.K, r);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dx[e] += r[e];
   }
-  store8_as<WHOLE>(a.dx_fmt, a.dX, row * a.lddx, c, lim, dx);
+  store8_as<MODE>(a.dx_fmt, a.dX, row * a.lddx, c, lim, dx);
 }
 
-template <int HF, int DF, int LPR, int VEC, bool WHOLE>
+template <int HF, int DF, int LPR, int VEC, int MODE>
 __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) {
   constexpr int RPB = NB_T / LPR;
   constexpr int hs = HF == FMT_F32 ? 4 : 2, ds = DF == FMT_F32 ? 4 : 2;
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
   const int64_t K = a.K;
   const float fk = (float)a.K;
   float gam[VEC][8], dg[VEC][8];
-  each_vector<WHOLE, VEC>([&](auto w, int j) {
+  each_vector<MODE, VEC>([&](auto w, int j) {
     load8_as<w()>(a.g_fmt, a.gamma, 0, (int64_t)(j * LPR + i) * 8, K, gam[j]);
 #pragma unroll
     for (int e = 0; e < 8; ++e) dg[j][e] = 0.f;
@@ -236,7 +235,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
   const auto request = [&](int64_t row) {
     const int64_t rd = min(row, a.rows - 1);       // past the end: the last row again, cleared below
     sn = a.rstd[rd];
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       const int64_t c = (int64_t)(j * LPR + i) * 8;
       hn[j] = row_raw8<HF, w()>(static_cast<const char*>(a.H) + rd * a.ldh * hs, c, K);
       dn[j] = row_raw8<DF, w()>(static_cast<const char*>(a.dY) + rd * a.lddy * ds, c, K);
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
     const bool live = row < a.rows;
     const float s = sn;
     float n[VEC][8], d[VEC][8];
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       const int64_t c = (int64_t)(j * LPR + i) * 8;
       row_val8<HF, w()>(hn[j], c, K, n[j]);
       row_val8<DF, w()>(dn[j], c, K, d[j]);
@@ -269,7 +268,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
       }
     if (!a.dX) continue;
     const float mean = row_sum<LPR>(dot, part[buf]) / fk;
-    each_vector<WHOLE, VEC>([&](auto w, int j) {
+    each_vector<MODE, VEC>([&](auto w, int j) {
       norm_dx8<w()>(a, row, (int64_t)(j * LPR + i) * 8, live ? K : 0, s, mean, n[j], d[j], gam[j]);
     });
   }
@@ -307,12 +306,12 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward(const NormBwdArgs a) 
       for (int e = 0; e < 8; ++e) dg[j][e] = comb[(j * LPR + i) * 8 + e];
   }
   const int64_t pitch = (K + 3) & ~3ll;
-  each_vector<WHOLE, VEC>([&](auto w, int j) {
+  each_vector<MODE, VEC>([&](auto w, int j) {
     row_store8<FMT_F32, w()>(a.ws + blockIdx.x * pitch, (int64_t)(j * LPR + i) * 8, K, dg[j]);
   });
 }
 
-// Rows of any length: one row per workgroup, read twice; a workgroup's sums for
+// Rows of any length: one per workgroup, read twice; a workgroup's sums for
 // dgamma live in its part of the workspace (each thread reads and writes its own
 // columns only).
 template <int HF, int DF>
@@ -331,7 +330,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward_long(const NormBwdArg
       float n[8], d[8], g[8];
       row_load8<HF>(hp, c, K, n);
       row_load8<DF>(dp, c, K, d);
-      load8_as<false>(a.g_fmt, a.gamma, 0, c, K, g);
+      load8_as<ROW_ANY>(a.g_fmt, a.gamma, 0, c, K, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) dot = fmaf(d[e] * g[e], n[e] * s, dot);
     }
@@ -340,7 +339,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward_long(const NormBwdArg
       float n[8], d[8], g[8];
       row_load8<HF>(hp, c, K, n);
       row_load8<DF>(dp, c, K, d);
-      load8_as<false>(a.g_fmt, a.gamma, 0, c, K, g);
+      load8_as<ROW_ANY>(a.g_fmt, a.gamma, 0, c, K, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) n[e] *= s;
       if (a.dgamma) {
@@ -350,7 +349,7 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward_long(const NormBwdArg
         for (int e = 0; e < 8; ++e) t[e] = fmaf(d[e], n[e], t[e]);
         row_store8<FMT_F32>(ws, c, K, t);
       }
-      if (a.dX) norm_dx8<false>(a, row, c, K, s, mean, n, d, g);
+      if (a.dX) norm_dx8<ROW_ANY>(a, row, c, K, s, mean, n, d, g);
     }
   }
 }
@@ -379,8 +378,8 @@ __global__ void __launch_bounds__(NT) k_norm_dgamma(const NormBwdArgs a) {
 }
 
 // ------------------------------------------------------------------------
-// Launchers.  Rows of up to 16384 columns are held in registers, in the smallest
-// (LPR, VEC) whose LPR * VEC * 8 columns hold one; longer rows are read twice.
+// Launchers.  Rows of 8 to 16384 columns are held in registers, in the smallest
+// (LPR, VEC) whose LPR * VEC * 8 columns hold one; others are read twice.
 // ------------------------------------------------------------------------
 constexpr int64_t NORM_REG_COLS = 16384;
 #define FORGE_NORM_SHAPES(X) X(16, 1) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(1024, 1) X(1024, 2)
@@ -392,10 +391,10 @@ static hipError_t launch_fwd(const NormArgs& a, hipStream_t st) {
     return dim3((unsigned)std::min<int64_t>((a.rows + rpb - 1) / rpb, 256 * (2048 / threads)));
   };
 #define FORGE_NORM(LPR, VEC)                                                                           \
-  if (a.K <= LPR * VEC * 8) {                                                                          \
+  if (a.K >= 8 && a.K <= LPR * VEC * 8) {                                                                          \
     constexpr int T = norm_threads(LPR);                                                               \
-    if (a.K % 8 == 0) hipLaunchKernelGGL((k_rmsnorm<XF, RF, LPR, VEC, true>), grid(T, T / LPR), dim3(T), 0, st, a); \
-    else hipLaunchKernelGGL((k_rmsnorm<XF, RF, LPR, VEC, false>), grid(T, T / LPR), dim3(T), 0, st, a); \
+    if (a.K % 8 == 0) hipLaunchKernelGGL((k_rmsnorm<XF, RF, LPR, VEC, ROW_WHOLE>), grid(T, T / LPR), dim3(T), 0, st, a); \
+    else hipLaunchKernelGGL((k_rmsnorm<XF, RF, LPR, VEC, ROW_BIG>), grid(T, T / LPR), dim3(T), 0, st, a); \
     return hipGetLastError();                                                                          \
   }
   FORGE_NORM_SHAPES(FORGE_NORM)
@@ -416,7 +415,7 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
 static int norm_bwd_lpr(int64_t K) { return K <= 128 ? 16 : K <= 1024 ? 64 : K <= 4096 ? 256 : 1024; }
 
 int norm_parts(int64_t rows, int64_t K) {
-  if (K > NORM_REG_COLS) return (int)std::min<int64_t>(rows, NB_LONG_PARTS);
+  if (K < 8 || K > NORM_REG_COLS) return (int)std::min<int64_t>(rows, NB_LONG_PARTS);
   const int64_t rpb = NB_T / norm_bwd_lpr(K), groups = (rows + rpb - 1) / rpb;
   // a part costs 8 bytes per column: beyond one per CU only where it has four rows to itself
   return (int)std::min<int64_t>(groups, std::max<int64_t>(256, std::min<int64_t>(groups / 4, NB_MAX_PARTS)));
@@ -426,9 +425,9 @@ template <int HF, int DF>
 static hipError_t launch_bwd(const NormBwdArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)a.parts), b(NB_T);
 #define FORGE_NORM_BWD(LPR, VEC)                                                                         \
-  if (a.K <= LPR * VEC * 8) {                                                                            \
-    if (a.K % 8 == 0) hipLaunchKernelGGL((k_rmsnorm_backward<HF, DF, LPR, VEC, true>), grid, b, 0, st, a); \
-    else hipLaunchKernelGGL((k_rmsnorm_backward<HF, DF, LPR, VEC, false>), grid, b, 0, st, a);           \
+  if (a.K >= 8 && a.K <= LPR * VEC * 8) {                                                                            \
+    if (a.K % 8 == 0) hipLaunchKernelGGL((k_rmsnorm_backward<HF, DF, LPR, VEC, ROW_WHOLE>), grid, b, 0, st, a); \
+    else hipLaunchKernelGGL((k_rmsnorm_backward<HF, DF, LPR, VEC, ROW_BIG>), grid, b, 0, st, a);           \
     return hipGetLastError();                                                                            \
   }
   FORGE_NORM_SHAPES(FORGE_NORM_BWD)

@@ -6,12 +6,13 @@ namespace forge {
 FORGE_ACT8_LIST(FORGE_INSTANTIATE_ACT8)
 
 // Gradient accumulation: a.dW (fp32) = G, or += G with a.dw_add.
+template <int MODE>
 __global__ void __launch_bounds__(NT, 2) k_gemm_act8(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
   int ti, tj;
   tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
   const int row0 = ti * TILE, col0 = tj * TILE;
-  tile_gradient_by<MainAct8>(a, lds, row0, col0);
+  tile_gradient_by<MainAct8<MODE>>(a, lds, row0, col0);
   const float* sG = reinterpret_cast<const float*>(lds);
   const int cl = 8 * (threadIdx.x & 15);
   const int64_t c = col0 + cl;
@@ -33,7 +34,8 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8(const KArgs8 a) {
 }
 
 hipError_t launch_gemm_act8(const KArgs8& a, hipStream_t st) {
-  hipLaunchKernelGGL(k_gemm_act8, tile_grid(a), dim3(NT), 0, st, a);
+  if (a.N >= 8 && a.K >= 8) hipLaunchKernelGGL((k_gemm_act8<ROW_BIG>), tile_grid(a), dim3(NT), 0, st, a);
+  else hipLaunchKernelGGL((k_gemm_act8<ROW_ANY>), tile_grid(a), dim3(NT), 0, st, a);
   return hipGetLastError();
 }
 

@@ -21,7 +21,8 @@ __device__ __forceinline__ u32x4 act8_bf16x8(u32x2 w, float f) {
 }
 
 // Any shape and alignment: MainBF16 with its register staging, X decoded on the
-// way into LDS.
+// way into LDS.  MODE: ROW_BIG where N and K are at least 8, else ROW_ANY.
+template <int MODE>
 struct MainAct8 {
   static constexpr int TK = MainBF16::TK;
   static constexpr int OPB = MainBF16::OPB;
@@ -46,8 +47,8 @@ struct MainAct8 {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int64_t tok = min(tok0 + 16 * r, a.BT - 1);   // past the end: read again, cleared in store()
-      ra[r] = row_raw8<FMT_BF16>(static_cast<const uint16_t*>(a.dY) + tok * a.lddy, cy, a.N);
-      rc[r] = codes_raw8(a.x8.codes + tok * a.x8.ld, cx, a.K);
+      ra[r] = row_raw8<FMT_BF16, MODE>(static_cast<const uint16_t*>(a.dY) + tok * a.lddy, cy, a.N);
+      rc[r] = codes_raw8<MODE>(a.x8.codes + tok * a.x8.ld, cx, a.K);
       rs[r] = (uint32_t)a.x8.scale[tok * a.x8.nb + (min(cx, (int64_t)a.K - 1) >> a.x8.sh)];
     }
   }
@@ -60,9 +61,9 @@ struct MainAct8 {
       const int t = (tid >> 4) + 16 * r;
       const bool in = tok0 + 16 * r < BT;
       float y[8];
-      row_val8<FMT_BF16>(ra[r], in ? cy : N, N, y);
+      row_val8<FMT_BF16, MODE>(ra[r], in ? cy : N, N, y);
       const u32x4 w = {bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7])};
-      const u32x2 c = codes_val8(rc[r], in ? cx : K, K);
+      const u32x2 c = codes_val8<MODE>(rc[r], in ? cx : K, K);
       const float s = act8_mul(in ? rs[r] : 0u);   // (a cleared code times a NaN scale would be a NaN)
       *reinterpret_cast<u32x4*>(stage + MainBF16::off(t, f)) = w;
       *reinterpret_cast<u32x4*>(stage + OPB + MainBF16::off(t, f)) =
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_wide(const KArgs8 a) {
   }
 }
 
-// Any shape.  ANY: rows of at least 4 elements (the epilogue's vectors at any alignment).
+// Any shape.  ANY: rows of dY, X and the state of at least 8 elements (vectors at any alignment).
 template <int OPT, int WF, int MF, int VF, bool ANY>
 __global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
   const int row0 = ti * TILE, col0 = tj * TILE;
   Epilogue<Step<OPT, WF, MF, VF, false, 0, ANY>, FMT_NONE, false, 4> epi;
   epi.tid = threadIdx.x;
-  tile_gradient_by<MainAct8>(a, lds, row0, col0);
+  tile_gradient_by<MainAct8<ANY ? ROW_BIG : ROW_ANY>>(a, lds, row0, col0);
   epi.prefetch(a, row0, col0);
   epi.run_prefetched(a, reinterpret_cast<const float*>(lds), row0, col0);
 }
@@ -567,7 +568,7 @@ hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st) {
     return a.x_fmt == FMT_S8 ? fused_act8_dma<FMT_S8, O, M, V>(a, w_fmt, st)
                              : fused_act8_dma<FMT_E4M3, O, M, V>(a, w_fmt, st);
 #define FORGE_ACT8(WF)                                                                                          \
-  if (a.K >= 4) hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, true>), tile_grid(a), dim3(NT), 0, st, a);        \
+  if (a.N >= 8 && a.K >= 8) hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, true>), tile_grid(a), dim3(NT), 0, st, a); \
   else hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, false>), tile_grid(a), dim3(NT), 0, st, a);
   if (w_fmt == FMT_BF16) { FORGE_ACT8(FMT_BF16) } else { FORGE_ACT8(FMT_F32) }
 #undef FORGE_ACT8
