@@ -130,31 +130,45 @@ __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t 
   return r;
 }
 
-template <int FMT, int MODE = ROW_ANY>
-__device__ __forceinline__ void row_val8(Raw8<FMT> r, int64_t c, int64_t K, float (&x)[8]) {
-  if constexpr (MODE != ROW_WHOLE) {
-    // elements the load began too early (rows shorter than 8 begin at 0: nothing to shift for c = 0)
-    const int s = MODE == ROW_BIG || K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
-    if constexpr (FMT == FMT_F32) {
-      const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-      r.a = s & 4 ? r.b : r.a;
-      r.b = s & 4 ? z : r.b;
-      r.a = s & 2 ? f32x4{r.a[2], r.a[3], r.b[0], r.b[1]} : r.a;
-      r.b = s & 2 ? f32x4{r.b[2], r.b[3], 0.f, 0.f} : r.b;
-      r.a = s & 1 ? f32x4{r.a[1], r.a[2], r.a[3], r.b[0]} : r.a;
-      r.b = s & 1 ? f32x4{r.b[1], r.b[2], r.b[3], 0.f} : r.b;
-      r.a = s & 8 ? z : r.a;
-      r.b = s & 8 ? z : r.b;
-    } else {
-      const u32x4 z = {0u, 0u, 0u, 0u};
-      r.a = s & 4 ? u32x4{r.a[2], r.a[3], 0u, 0u} : r.a;
-      r.a = s & 2 ? u32x4{r.a[1], r.a[2], r.a[3], 0u} : r.a;
-      r.a = s & 1 ? u32x4{(r.a[0] >> 16) | (r.a[1] << 16), (r.a[1] >> 16) | (r.a[2] << 16),
-                          (r.a[2] >> 16) | (r.a[3] << 16), r.a[3] >> 16}
-                  : r.a;
-      r.a = s & 8 ? z : r.a;
-    }
+// 8 elements moved down by s places (0 .. 7; 8: all cleared), zeros above.
+template <int FMT>
+__device__ __forceinline__ Raw8<FMT> raw_shift8(Raw8<FMT> r, int s) {
+  if constexpr (FMT == FMT_F32) {
+    const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+    r.a = s & 4 ? r.b : r.a;
+    r.b = s & 4 ? z : r.b;
+    r.a = s & 2 ? f32x4{r.a[2], r.a[3], r.b[0], r.b[1]} : r.a;
+    r.b = s & 2 ? f32x4{r.b[2], r.b[3], 0.f, 0.f} : r.b;
+    r.a = s & 1 ? f32x4{r.a[1], r.a[2], r.a[3], r.b[0]} : r.a;
+    r.b = s & 1 ? f32x4{r.b[1], r.b[2], r.b[3], 0.f} : r.b;
+    r.a = s & 8 ? z : r.a;
+    r.b = s & 8 ? z : r.b;
+  } else {
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    r.a = s & 4 ? u32x4{r.a[2], r.a[3], 0u, 0u} : r.a;
+    r.a = s & 2 ? u32x4{r.a[1], r.a[2], r.a[3], 0u} : r.a;
+    r.a = s & 1 ? u32x4{(r.a[0] >> 16) | (r.a[1] << 16), (r.a[1] >> 16) | (r.a[2] << 16),
+                        (r.a[2] >> 16) | (r.a[3] << 16), r.a[3] >> 16}
+                : r.a;
+    r.a = s & 8 ? z : r.a;
   }
+  return r;
+}
+// Elements that the load of row_raw8 began too early, 8 from K on (rows shorter than 8
+// begin at 0: nothing to shift for c = 0).
+template <int MODE = ROW_ANY>
+__device__ __forceinline__ int row_early8(int64_t c, int64_t K) {
+  return MODE == ROW_BIG || K >= 8 ? (int)min((int64_t)8, c - min(c, K - 8)) : c > 0 ? 8 : 0;
+}
+// The loaded elements in their places, as stored.
+template <int FMT, int MODE = ROW_ANY>
+__device__ __forceinline__ Raw8<FMT> row_place8(const Raw8<FMT>& r, int64_t c, int64_t K) {
+  if constexpr (MODE == ROW_WHOLE) return r;
+  else return raw_shift8<FMT>(r, row_early8<MODE>(c, K));
+}
+template <int FMT, int MODE = ROW_ANY>
+__device__ __forceinline__ void row_val8(const Raw8<FMT>& raw, int64_t c, int64_t K, float (&x)[8]) {
+  const Raw8<FMT> r = row_place8<FMT, MODE>(raw, c, K);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if constexpr (FMT == FMT_F32) {

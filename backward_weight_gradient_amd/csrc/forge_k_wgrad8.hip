@@ -5,19 +5,13 @@ namespace forge {
 
 FORGE_ACT8_LIST(FORGE_INSTANTIATE_ACT8)
 
-// Gradient accumulation: a.dW (fp32) = G, or += G with a.dw_add.
-template <int MODE>
-__global__ void __launch_bounds__(NT, 2) k_gemm_act8(const KArgs8 a) {
-  __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
-  int ti, tj;
-  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
-  const int row0 = ti * TILE, col0 = tj * TILE;
-  tile_gradient_by<MainAct8<MODE>>(a, lds, row0, col0);
-  const float* sG = reinterpret_cast<const float*>(lds);
+// Gradient accumulation: a.dW (fp32) = G, or += G with a.dw_add, from a G tile in LDS.
+template <int ROWS, int THREADS>
+__device__ __forceinline__ void store_g(const KArgs8& a, const float* sG, int row0, int col0) {
   const int cl = 8 * (threadIdx.x & 15);
   const int64_t c = col0 + cl;
 #pragma unroll 4
-  for (int r = threadIdx.x >> 4; r < TILE; r += NT / 16) {
+  for (int r = threadIdx.x >> 4; r < ROWS; r += THREADS / 16) {
     if (row0 + r >= a.N) return;
     float* out = static_cast<float*>(a.dW) + (int64_t)(row0 + r) * a.lddw;
     float g[8];
@@ -33,9 +27,46 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8(const KArgs8 a) {
   }
 }
 
+template <int XF>
+__global__ void __launch_bounds__(NT, 2) k_gemm_act8_dma(const KArgs8 a) {
+  __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
+  int ti, tj;
+  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
+  f32x16 acc[2][2];
+  Act8Loop<XF, 4, 2> loop;
+  loop.run(a, lds, ti * TILE, tj * TILE, acc);
+  bar();   // every wave is done with the stages before G overwrites them
+  float* sG = reinterpret_cast<float*>(lds);
+  store_acc(sG, acc, threadIdx.x);
+  __syncthreads();
+  store_g<TILE, NT>(a, sG, ti * TILE, tj * TILE);
+}
+
+__global__ void __launch_bounds__(2 * NT, 1) k_gemm_act8_split(const KArgs8 a) {
+  __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
+  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  f32x16 acc[2][4];
+  if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);
+  else Act8Split::run<FMT_E4M3>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);
+  float* sG = reinterpret_cast<float*>(lds);
+  Act8Split::join(sG, acc);
+  store_g<SPLIT_ROWS, 2 * NT>(a, sG, ti * SPLIT_ROWS, tj * TILE);
+}
+
+__global__ void __launch_bounds__(NT, 2) k_gemm_act8_tiny(const KArgs8 a) {
+  __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
+  int ti, tj;
+  tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
+  tile_gradient_by<MainAct8>(a, lds, ti * TILE, tj * TILE);
+  store_g<TILE, NT>(a, reinterpret_cast<const float*>(lds), ti * TILE, tj * TILE);
+}
+
+// The same choice as for the step (the accumulator's rows may be of any alignment).
 hipError_t launch_gemm_act8(const KArgs8& a, hipStream_t st) {
-  if (a.N >= 8 && a.K >= 8) hipLaunchKernelGGL((k_gemm_act8<ROW_BIG>), tile_grid(a), dim3(NT), 0, st, a);
-  else hipLaunchKernelGGL((k_gemm_act8<ROW_ANY>), tile_grid(a), dim3(NT), 0, st, a);
+  if (act8_split(a, a.x_dma)) hipLaunchKernelGGL(k_gemm_act8_split, split_grid(a), dim3(2 * NT), 0, st, a);
+  else if (a.x_dma && a.x_fmt == FMT_S8) hipLaunchKernelGGL((k_gemm_act8_dma<FMT_S8>), tile_grid(a), dim3(NT), 0, st, a);
+  else if (a.x_dma) hipLaunchKernelGGL((k_gemm_act8_dma<FMT_E4M3>), tile_grid(a), dim3(NT), 0, st, a);
+  else hipLaunchKernelGGL(k_gemm_act8_tiny, tile_grid(a), dim3(NT), 0, st, a);
   return hipGetLastError();
 }
 

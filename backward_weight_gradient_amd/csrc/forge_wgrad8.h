@@ -3,8 +3,8 @@
 // G = dY^T X with X = code * 2^e.  The exponent differs from token to token, so
 // it cannot leave the sum; each 8 bits are decoded to the bf16 they stand for
 // (exactly) between global memory and LDS, after which the matrix-core loop is
-// that of bf16 inputs: every element of G sees the same MFMA sequence as with
-// the decoded X, and the results are the same bit for bit.
+// that of bf16 inputs.  In the kernels of aligned layers every element of G sees the
+// same MFMA sequence as with the decoded X, so the results are the same bit for bit.
 #pragma once
 
 #include "forge_act8.h"
@@ -20,10 +20,10 @@ __device__ __forceinline__ u32x4 act8_bf16x8(u32x2 w, float f) {
   return u32x4{bf16x2_rne(x[0], x[1]), bf16x2_rne(x[2], x[3]), bf16x2_rne(x[4], x[5]), bf16x2_rne(x[6], x[7])};
 }
 
-// Any shape and alignment: MainBF16 with its register staging, X decoded on the
-// way into LDS.  MODE: ROW_BIG where N and K are at least 8, else ROW_ANY.
-template <int MODE>
+// Layers with fewer than 8 outputs or 16 inputs: MainBF16 with its register staging,
+// X decoded on the way into LDS.
 struct MainAct8 {
+  static constexpr int MODE = ROW_ANY;
   static constexpr int TK = MainBF16::TK;
   static constexpr int OPB = MainBF16::OPB;
   static constexpr int STAGE = MainBF16::STAGE;
@@ -60,9 +60,7 @@ struct MainAct8 {
     for (int r = 0; r < 4; ++r) {
       const int t = (tid >> 4) + 16 * r;
       const bool in = tok0 + 16 * r < BT;
-      float y[8];
-      row_val8<FMT_BF16, MODE>(ra[r], in ? cy : N, N, y);
-      const u32x4 w = {bf16x2_rne(y[0], y[1]), bf16x2_rne(y[2], y[3]), bf16x2_rne(y[4], y[5]), bf16x2_rne(y[6], y[7])};
+      const u32x4 w = row_place8<FMT_BF16, MODE>(ra[r], in ? cy : N, N).a;
       const u32x2 c = codes_val8<MODE>(rc[r], in ? cx : K, K);
       const float s = act8_mul(in ? rs[r] : 0u);   // (a cleared code times a NaN scale would be a NaN)
       *reinterpret_cast<u32x4*>(stage + MainBF16::off(t, f)) = w;
@@ -517,18 +515,209 @@ __global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_wide(const KArgs8 a) {
   }
 }
 
-// Any shape.  ANY: rows of dY, X and the state of at least 8 elements (vectors at any alignment).
-template <int OPT, int WF, int MF, int VF, bool ANY>
-__global__ void __launch_bounds__(NT, 2) k_fused_act8(const KArgs8 a) {
+// ------------------------------------------------------------------------
+// Few tiles, or rows the ring does not take (N >= 8, K >= 16): the token axis split
+// over the 8 waves of a workgroup.  A tile is 64
+// rows x 128 columns; wave w takes the 32-token chunks w, w + 8, .. alone, with a
+// slab of LDS of its own (so its loop has no barrier), and the 8 sums are added in
+// a fixed order at the end.  Any alignment: rows are loaded into registers a chunk
+// ahead, the vector that a row ends in shifted into place.
+// LDS: 8 slabs of 12 KiB (dY 32 x 64, X 32 x 128, bf16), then 4 G tiles over them.
+// ------------------------------------------------------------------------
+constexpr int SPLIT_ROWS = 64, SPLIT_WAVES = 8;
+constexpr int SPLIT_DY = 32 * SPLIT_ROWS * 2, SPLIT_SLAB = SPLIT_DY + 32 * TILE * 2;
+constexpr int SPLIT_G = SPLIT_ROWS * GP;                     // floats of one G tile
+constexpr int LDS_SPLIT = 4 * SPLIT_G * 4;
+static_assert(SPLIT_WAVES * SPLIT_SLAB <= LDS_SPLIT && LDS_SPLIT <= 160 * 1024, "LDS budget");
+
+// 16 codes at column c of a row of K >= 16: the load of those at min(c, K - 16), and
+// what moves them into place.
+__device__ __forceinline__ u32x4 codes_raw16(const uint8_t* p, int64_t c, int64_t K) {
+  typedef uint32_t u32x4_c __attribute__((ext_vector_type(4), aligned(1)));
+  return *reinterpret_cast<const u32x4_c*>(p + min(c, K - 16));
+}
+__device__ __forceinline__ u32x4 codes_shift16(u32x4 w, int s) {   // down by s places (0 .. 15)
+  w = s & 8 ? u32x4{w[2], w[3], 0u, 0u} : w;
+  w = s & 4 ? u32x4{w[1], w[2], w[3], 0u} : w;
+  return u32x4{__builtin_amdgcn_alignbyte(w[1], w[0], s & 3), __builtin_amdgcn_alignbyte(w[2], w[1], s & 3),
+               __builtin_amdgcn_alignbyte(w[3], w[2], s & 3), w[3] >> (8 * (s & 3))};
+}
+
+struct Act8Split {
+  // byte offset of (token, feature) in the dY half of a slab: 128-byte rows, every
+  // other pair of rows shifted by 64 bytes, so that the 4 rows of a transposing read
+  // lie in different banks (X's rows: MainBF16::off)
+  __device__ __forceinline__ static int off_dy(int t, int f) { return t * (SPLIT_ROWS * 2) + ((f * 2) ^ ((t & 2) << 5)); }
+
+  __device__ __forceinline__ static bf16x8 frag(const char* lo, int hi) {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)lo);
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(lo + hi));
+    const s16x4 both[2] = {a, b};
+    return __builtin_bit_cast(bf16x8, both);
+  }
+
+  template <int XF>
+  __device__ __forceinline__ static void run(const KArgs8& a, char* lds, int row0, int col0, f32x16 (&acc)[2][4]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    char* slab = lds + wave * SPLIT_SLAB;
+#pragma unroll
+    for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+      for (int bj = 0; bj < 4; ++bj)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
+    const int nk = (a.BT + 31) / 32;
+    const int t0 = lane >> 3;                      // tokens t0 + 8 r of a chunk
+    const int64_t cy = row0 + 8 * (lane & 7), cx = col0 + 16 * (lane & 7);
+    const int64_t sx = min(cx, (int64_t)a.K - 1) >> a.x8.sh;
+    Raw8<FMT_BF16> ry[4];
+    u32x4 rx[4];
+    uint32_t rs[4];
+    const auto request = [&](int kc) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t tok = min((int64_t)kc * 32 + t0 + 8 * r, (int64_t)a.BT - 1);   // past the end: read again, cleared below
+        ry[r] = row_raw8<FMT_BF16, ROW_BIG>(static_cast<const uint16_t*>(a.dY) + tok * a.lddy, cy, a.N);
+        rx[r] = codes_raw16(a.x8.codes + tok * a.x8.ld, cx, a.K);
+        rs[r] = (uint32_t)a.x8.scale[tok * a.x8.nb + sx];
+      }
+    };
+    const int tl = 8 * (lane >> 5) + ((lane & 15) >> 2), fl = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+    if (wave < nk) request(wave);
+    // Only the vectors that a row ends in need moving; one wholly past the end holds
+    // other columns' values, which reach nothing but elements of G that are not stored.
+    const bool move = (row0 + SPLIT_ROWS > a.N && (a.N & 7)) || (col0 + TILE > a.K && (a.K & 15));
+    const int ey = (int)min((int64_t)7, cy - min(cy, (int64_t)a.N - 8)), ex = (int)min((int64_t)15, cx - min(cx, (int64_t)a.K - 16));
+    for (int kc = wave; kc < nk; kc += SPLIT_WAVES) {
+      if (move) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          ry[r] = raw_shift8<FMT_BF16>(ry[r], ey);
+          rx[r] = codes_shift16(rx[r], ex);
+        }
+      }
+      if (kc * 32 + 32 > a.BT) {   // tokens past the end
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (kc * 32 + t0 + 8 * r >= a.BT) {
+            ry[r].a = rx[r] = u32x4{0u, 0u, 0u, 0u};
+            rs[r] = 0u;
+          }
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int t = t0 + 8 * r;
+        *reinterpret_cast<u32x4*>(slab + off_dy(t, 8 * (lane & 7))) = ry[r].a;
+        const float f = act8_mul(rs[r]);
+        char* x = slab + SPLIT_DY + MainBF16::off(t, 16 * (lane & 7));
+        *reinterpret_cast<u32x4*>(x) = act8_bf16x8<XF>(u32x2{rx[r][0], rx[r][1]}, f);
+        *reinterpret_cast<u32x4*>(x + 16) = act8_bf16x8<XF>(u32x2{rx[r][2], rx[r][3]}, f);
+      }
+      if (kc + SPLIT_WAVES < nk) request(kc + SPLIT_WAVES);
+      // the wave's own LDS writes before its lanes' reads (the hardware runs a wave's
+      // LDS accesses in order)
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        bf16x8 fa[2], fb[4];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) fa[b] = frag(slab + off_dy(tl, b * 32 + fl) + ks * 16 * SPLIT_ROWS * 2, 4 * SPLIT_ROWS * 2);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          fb[b] = frag(slab + SPLIT_DY + MainBF16::off(tl, b * 32 + fl) + ks * 16 * TILE * 2, 4 * TILE * 2);
+#pragma unroll
+        for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+          for (int bj = 0; bj < 4; ++bj)
+            acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[bi], fb[bj], acc[bi][bj], 0, 0, 0);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+
+  // The sum of the 8 waves' tiles into the first G tile of LDS: waves 0 - 3 write
+  // theirs, waves 4 - 7 add theirs to those, and the threads add the four.
+  __device__ __forceinline__ static void join(float* sG, const f32x16 (&acc)[2][4]) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float* mine = sG + (wave & 3) * SPLIT_G;
+    __syncthreads();                             // the slabs are no longer read
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (wave >> 2 == h) {
+#pragma unroll
+        for (int bi = 0; bi < 2; ++bi)
+#pragma unroll
+          for (int bj = 0; bj < 4; ++bj)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float* p = mine + (bi * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3)) * GP + bj * 32 + (lane & 31);
+              *p = h == 0 ? acc[bi][bj][e] : *p + acc[bi][bj][e];
+            }
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = threadIdx.x; i < SPLIT_ROWS * TILE / 4; i += 2 * NT) {
+      float* p = sG + (i >> 5) * GP + 4 * (i & 31);
+      f32x4 g = *reinterpret_cast<f32x4*>(p);
+#pragma unroll
+      for (int k = 1; k < 4; ++k) g += *reinterpret_cast<f32x4*>(p + k * SPLIT_G);
+      *reinterpret_cast<f32x4*>(p) = g;
+    }
+    __syncthreads();
+  }
+};
+
+template <int OPT, int WF, int MF, int VF>
+__global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_split(const KArgs8 a) {
+  __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
+  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  const int row0 = ti * SPLIT_ROWS, col0 = tj * TILE;
+  f32x16 acc[2][4];
+  if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, row0, col0, acc);
+  else Act8Split::run<FMT_E4M3>(a, lds, row0, col0, acc);
+  Epilogue<Step<OPT, WF, MF, VF, false, 0, true>, FMT_NONE, false, 2, 2 * NT, false, false, SPLIT_ROWS> epi;
+  epi.tid = threadIdx.x;
+  epi.prefetch(a, row0, col0);
+  float* sG = reinterpret_cast<float*>(lds);
+  Act8Split::join(sG, acc);
+  epi.run_prefetched(a, sG, row0, col0);
+}
+
+template <int OPT, int WF, int MF, int VF>
+__global__ void __launch_bounds__(NT, 2) k_fused_act8_tiny(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_BYTES];
   int ti, tj;
   tile_coords(blockIdx.x, a.tiles_n, a.tiles_k, ti, tj);
   const int row0 = ti * TILE, col0 = tj * TILE;
-  Epilogue<Step<OPT, WF, MF, VF, false, 0, ANY>, FMT_NONE, false, 4> epi;
+  Epilogue<Step<OPT, WF, MF, VF, false>, FMT_NONE, false, 4> epi;
   epi.tid = threadIdx.x;
-  tile_gradient_by<MainAct8<ANY ? ROW_BIG : ROW_ANY>>(a, lds, row0, col0);
+  tile_gradient_by<MainAct8>(a, lds, row0, col0);
   epi.prefetch(a, row0, col0);
   epi.run_prefetched(a, reinterpret_cast<const float*>(lds), row0, col0);
+}
+
+// Which kernel takes a layer (measured with AdamW, fp32 moments):
+//  - the ring of 128 x 128 tiles (k_fused_act8_dma) needs aligned rows in whole 16-byte
+//    segments, and enough tiles: with 128 of them (1024 x 2048) it takes 16.0 / 26.8 /
+//    59.9 us at BT 256 / 1024 / 4096, the split kernel 12.4 / 17.9 / 34.9; with 256
+//    (2048 x 2048) 21.1 / 31.7 / 65.4 against 23.3 / 32.7 / 65.9; below BT 128 the
+//    split kernel's joining costs more than it saves (64 x 64: 8.5 against 5.8 us);
+//  - the 256 x 256 tiles (k_fused_act8_wide) pay for long token axes once they fill the
+//    chip: at BT 8192 239 against 302 us for 256 of them (4096 x 4096), but 212
+//    against 109 for 64 (2048 x 2048);
+//  - everything else of at least 8 x 16 is the split kernel's (3000 x 3000, whose rows
+//    the ring does not take: 290 us at BT 8192, 527 through registers).
+inline bool act8_ring(const KArgs8& a) { return a.x_dma && a.vec_state && a.K % 4 == 0; }
+inline bool act8_split(const KArgs8& a, bool ring) {
+  return a.N >= 8 && a.K >= 16 && (!ring || ((int64_t)a.tiles_n * a.tiles_k < 256 && a.BT >= 128));
+}
+inline bool act8_wide(const KArgs8& a) {
+  return a.BT >= WIDE_MIN_BT && (int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) >= 192;
+}
+inline dim3 split_grid(const KArgs8& a) {
+  return dim3((unsigned)((a.N + SPLIT_ROWS - 1) / SPLIT_ROWS * a.tiles_k));
 }
 
 template <int XF, int O, int M, int V>
@@ -536,7 +725,7 @@ hipError_t fused_act8_dma(const KArgs8& a, int w_fmt, hipStream_t st) {
 #define FORGE_ACT8_DMA(WF, BLK, FULL)                                                                                 \
   hipLaunchKernelGGL((k_fused_act8_dma<XF, O, WF, M, V, BLK, FULL>), tile_grid(a), dim3(NT), 0, st, a);               \
   return hipGetLastError();
-  if (a.BT >= WIDE_MIN_BT) {   // (combo_fused's variants)
+  if (act8_wide(a)) {   // (combo_fused's variants)
     const dim3 g((unsigned)(((a.N + 255) / 256) * ((a.K + 255) / 256)));
     if constexpr (full_pays(M, V)) {
       if (whole_tiles(a) && w_fmt == FMT_BF16) {
@@ -564,14 +753,18 @@ hipError_t fused_act8_dma(const KArgs8& a, int w_fmt, hipStream_t st) {
 template <int O, int M, int V>
 hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st) {
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
-  if (a.x_dma && a.vec_state && a.K % 4 == 0)
+  const bool wbf = w_fmt == FMT_BF16, ring = act8_ring(a);
+  if (act8_split(a, ring)) {
+    if (wbf) hipLaunchKernelGGL((k_fused_act8_split<O, FMT_BF16, M, V>), split_grid(a), dim3(2 * NT), 0, st, a);
+    else hipLaunchKernelGGL((k_fused_act8_split<O, FMT_F32, M, V>), split_grid(a), dim3(2 * NT), 0, st, a);
+  } else if (ring) {
     return a.x_fmt == FMT_S8 ? fused_act8_dma<FMT_S8, O, M, V>(a, w_fmt, st)
                              : fused_act8_dma<FMT_E4M3, O, M, V>(a, w_fmt, st);
-#define FORGE_ACT8(WF)                                                                                          \
-  if (a.N >= 8 && a.K >= 8) hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, true>), tile_grid(a), dim3(NT), 0, st, a); \
-  else hipLaunchKernelGGL((k_fused_act8<O, WF, M, V, false>), tile_grid(a), dim3(NT), 0, st, a);
-  if (w_fmt == FMT_BF16) { FORGE_ACT8(FMT_BF16) } else { FORGE_ACT8(FMT_F32) }
-#undef FORGE_ACT8
+  } else if (wbf) {
+    hipLaunchKernelGGL((k_fused_act8_tiny<O, FMT_BF16, M, V>), tile_grid(a), dim3(NT), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((k_fused_act8_tiny<O, FMT_F32, M, V>), tile_grid(a), dim3(NT), 0, st, a);
+  }
   return hipGetLastError();
 }
 #define FORGE_INSTANTIATE_ACT8(O, M, V) \

@@ -417,7 +417,9 @@ forge_status forge_act_dequantize(const forge_act8* Q, forge_mat* X, void* strea
  * forge_wgrad_step_act8 -- forge_wgrad_step with X from its 8-bit copy (paper,
  * section 2.2 and Algorithm 1): the codes are decoded on their way into the
  * matrix cores, so G = dY^T (stored values) without X in 16 bits in memory.
- * The result equals forge_wgrad_step on the decoded BF16 X.
+ * G is the sum that forge_wgrad_step takes over the decoded BF16 X: for aligned
+ * layers that fill the chip in the same order (the results are then the same bit
+ * for bit), else in another fixed order.
  * dY: [BT, N] BF16.  W: [N, K] BF16 or F32.  Supported: AdamW with (m, v) in
  * {(F32, F32), (BF16, BF16), (S8, U8), (E4M3, E4M3)}; Lion and SGD-m with m in
  * {F32, BF16}.  Any other optimizer: forge_wgrad_accumulate_act8, then
