@@ -991,12 +991,14 @@ __device__ __forceinline__ void ld4(Raw4<FMT>& r, const void* seg, const Seg& g,
 // access in any case, the segment that the row ends in read 4 - nv elements early
 // and shifted down by any_shift4 once it is decoded.  (With element-wise reads the
 // branches make each segment wait for its own loads.)  8-bit rows are whole blocks.
+// Accesses are cached ones here: such rows share lines with their neighbours, and
+// parts of lines that bypass the caches are moved twice.
 template <int FMT>
 __device__ __forceinline__ void ld4_any(Raw4<FMT>& r, const void* seg, const Seg& g) {
   const int early = 4 - g.nv;
-  if constexpr (FMT == FMT_F32) r.v = ld_nt<f32x4_e>(static_cast<const float*>(seg) - early);
-  else if constexpr (FMT == FMT_BF16) r.v = ld_nt<u32x2_e>(static_cast<const uint16_t*>(seg) - early);
-  else if constexpr (fmt_blocked(FMT)) r.v = ld_nt<u32_e>(seg);
+  if constexpr (FMT == FMT_F32) r.v = *reinterpret_cast<const f32x4_e*>(static_cast<const float*>(seg) - early);
+  else if constexpr (FMT == FMT_BF16) r.v = *reinterpret_cast<const u32x2_e*>(static_cast<const uint16_t*>(seg) - early);
+  else if constexpr (fmt_blocked(FMT)) r.v = *static_cast<const u32_e*>(seg);
 }
 __device__ __forceinline__ void any_shift4(float* x, const Seg& g) {
   const int early = 4 - g.nv;
@@ -1070,7 +1072,7 @@ __device__ __forceinline__ void st4(void* seg, const Seg& g, bool vec, const flo
   if constexpr (FMT == FMT_F32) {
     float* p = static_cast<float*>(seg);
     if (ANY && g.nv == 4) {
-      st_nt<f32x4_e>(p, f32x4_e{x[0], x[1], x[2], x[3]});
+      *reinterpret_cast<f32x4_e*>(p) = f32x4_e{x[0], x[1], x[2], x[3]};
     } else if (FAST || (vec && g.nv == 4)) {
       st_nt<f32x4>(p, f32x4{x[0], x[1], x[2], x[3]});
     } else {
@@ -1101,7 +1103,7 @@ __device__ __forceinline__ void st4(void* seg, const Seg& g, bool vec, const flo
     }
     uint16_t* p = static_cast<uint16_t*>(seg);
     if (ANY && g.nv == 4) {
-      st_nt<u32x2_e>(p, u32x2_e{lo, hi});
+      *reinterpret_cast<u32x2_e*>(p) = u32x2_e{lo, hi};
     } else if (FAST || (vec && g.nv == 4)) {
       st_nt<u32x2>(p, u32x2{lo, hi});
     } else {

@@ -97,7 +97,15 @@ __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const Embed
   __shared__ int rng[2 * ROWS];
   __shared__ float red[3 * TILE];
   constexpr int MODE = FAST || ANY ? ROW_BIG : ROW_ANY;
-  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  if (ANY) {          // 8 rows of tiles at a time, one to an XCD (workgroups go to the 8 in turn)
+    const int rows8 = (int)gridDim.x / (8 * a.tiles_k) * 8, b = (int)blockIdx.x;
+    if (b < rows8 * a.tiles_k) {
+      const int g = b / (8 * a.tiles_k);
+      ti = 8 * g + (b & 7);
+      tj = (b - 8 * g * a.tiles_k) >> 3;
+    }
+  }
   const int row0 = ti * ROWS, col0 = tj * TILE;
   Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, ROWS> epi;
   epi.tid = threadIdx.x;
@@ -108,18 +116,22 @@ __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const Embed
   epi.run_prefetched(a, sG, row0, col0);
 }
 
+// FAST: rows of whole 128-byte lines, whose accesses bypass the caches and whose
+// tiles go out row of tiles by row.  Other rows share lines at the tiles' seams, and
+// streaming parts of lines through different XCDs costs far more than the lines
+// themselves: 37929 x 2984 bf16 629 us so, 337 us with cached accesses and neighbouring
+// tiles on one XCD (46421 x 1459, fp32 state: 530 and 316).
+//
 // Tiles of 128 rows, or of 16 where those would be fewer than two per CU: then a
 // step is bound by the gathering of each tile's tokens, not by HBM.
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
-  const bool fast = a.vec_state && a.K % 4 == 0 && a.K >= 8;
+  const bool fast = a.vec_state && a.K % 64 == 0 && a.ldw % 64 == 0 && a.ldm % 64 == 0 && a.ldv % 64 == 0;
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
   const int64_t rows = (int64_t)a.tiles_n * a.tiles_k >= 512 && a.K >= 8 ? TILE : EMBED_MIN_ROWS;
   const int64_t tiles = (a.N + rows - 1) / rows;
-  if (e.T > 0) {
-    const hipError_t err = launch_embed_tiles(e, rows, tiles, st);
-    if (err != hipSuccess) return err;
-  }
+  const hipError_t err = launch_embed_sort(e, rows, tiles, st);
+  if (err != hipSuccess) return err;
   const dim3 grid((unsigned)(tiles * a.tiles_k));
 #define FORGE_EMBED(ROWS, FA, ANY)                                                                                          \
   if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<ROWS, FA, ANY, O, FMT_BF16, M, V>), grid, dim3(NT), 0, st, a, e); \

@@ -357,8 +357,8 @@ struct EmbedArgs {
 };
 hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
                         int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t stream);
-hipError_t launch_embed_sort(const EmbedArgs& e, hipStream_t stream);
-hipError_t launch_embed_tiles(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t stream);
+// The tokens sorted by id, and where each tile of `rows` rows begins and the last ends.
+hipError_t launch_embed_sort(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t stream);
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t stream);
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st);

@@ -20,14 +20,36 @@ __device__ __forceinline__ void load_ids(const void* ids, int id_bytes, F&& at, 
   }
 }
 
-// Zero a matrix of format fmt.
-__global__ void __launch_bounds__(NT) k_zero_rows(void* p, int64_t ld, int fmt, int64_t rows, int64_t K) {
-  const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-    for (int64_t c = (int64_t)threadIdx.x * 8; c < K; c += NT * 8) {
-      if (fmt == FMT_F32) row_store8<FMT_F32>(static_cast<float*>(p) + r * ld, c, K, z);
-      else row_store8<FMT_BF16>(static_cast<uint16_t*>(p) + r * ld, c, K, z);
+// Lanes of `each` columns that a row is spread over, as a power of two, at most 2^most.
+inline int lane_shift(int64_t K, int each, int most) {
+  int sh = 0;
+  while (sh < most && ((int64_t)each << sh) < K) ++sh;
+  return sh;
+}
+
+// Zero rows x K of format FMT: workgroup wg of wgs, each of nt threads, a row to 1 << sh
+// of them.  Bound by HBM; past the caches 128256 x 4096 fp32 are cleared at 6 TB/s
+// (through them at 5).
+struct ZeroArgs {
+  void* p; int64_t ld, rows, K;
+  int32_t sh;
+};
+template <int FMT>
+__device__ __forceinline__ void zero_rows(const ZeroArgs& z, int64_t wg, int64_t wgs, int nt) {
+  using E = std::conditional_t<FMT == FMT_F32, float, uint16_t>;
+  using E4 = std::conditional_t<FMT == FMT_F32, f32x4_e, u32x2_e>;
+  const int per = nt >> z.sh;
+  for (int64_t r = wg * per + (threadIdx.x >> z.sh); r < z.rows; r += wgs * per) {
+    E* p = static_cast<E*>(z.p) + r * z.ld;
+    for (int64_t c = (int64_t)(threadIdx.x & ((1 << z.sh) - 1)) * 4; c < z.K; c += (int64_t)4 << z.sh) {
+      if (c + 4 <= z.K) __builtin_nontemporal_store(E4{}, reinterpret_cast<E4*>(p + c));
+      else for (int64_t k = c; k < z.K; ++k) p[k] = E(0);
     }
+  }
+}
+template <int FMT>
+__global__ void __launch_bounds__(NT) k_zero_rows(const ZeroArgs z) {
+  zero_rows<FMT>(z, blockIdx.x, gridDim.x, NT);
 }
 
 // ------------------------------------------------------------------------
@@ -82,17 +104,16 @@ __global__ void __launch_bounds__(NT) k_embed(const LookupArgs a) {
 hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
                         int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t st) {
   if (T == 0 || K == 0) return hipSuccess;
+  const int sh = lane_shift(K, 8, 8), rows = NT >> sh;      // rows of a workgroup
   if (V == 0) {   // nothing but padding
-    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)std::min<int64_t>(T, 1 << 20)), dim3(NT), 0, st, Y, ldy, y_fmt, T, K);
+    const ZeroArgs z{Y, ldy, T, K, sh};
+    const dim3 g((unsigned)std::min<int64_t>((T + rows - 1) / rows, 1 << 20));
+    if (y_fmt == FMT_F32) hipLaunchKernelGGL(k_zero_rows<FMT_F32>, g, dim3(NT), 0, st, z);
+    else hipLaunchKernelGGL(k_zero_rows<FMT_BF16>, g, dim3(NT), 0, st, z);
     return hipGetLastError();
   }
-  LookupArgs a{ids, id_bytes, T, V, K, W, ldw, Y, ldy, scale, 0, 0, 0};
-  const int64_t lanes = (K + 7) / 8;
-  a.tsh = 0;
-  while (a.tsh < 8 && (1 << a.tsh) < lanes) ++a.tsh;
-  a.segs = (int32_t)((lanes + (1 << a.tsh) - 1) >> a.tsh);
-  const int64_t rpb = (int64_t)(NT >> a.tsh) * EMB_UNR;
-  a.units = ((T + rpb - 1) / rpb) * a.segs;
+  const int64_t segs = (K + ((int64_t)8 << sh) - 1) >> (sh + 3), per = (int64_t)rows * EMB_UNR;
+  const LookupArgs a{ids, id_bytes, T, V, K, W, ldw, Y, ldy, scale, sh, (int32_t)segs, (T + per - 1) / per * segs};
   const dim3 grid((unsigned)std::min<int64_t>(a.units, 1 << 22)), b(NT);
   const bool wf = w_fmt == FMT_F32, yf = y_fmt == FMT_F32;
 #define FORGE_LOOKUP(MODE)                                                                        \
@@ -110,63 +131,103 @@ hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W,
 // Tokens sorted by id, stable, without atomics.
 //  k_embed_place: each token's place within its part of EMBED_PART tokens, by
 //    counting: place(i) = #{j: row_j < row_i} + #{j < i: row_j = row_i}.  A workgroup
-//    places 16 tokens against the whole part in LDS, 16 threads a token; two
-//    instructions a pair.  Quadratic, but spread over the whole chip: 8192 tokens
-//    are 67 M pairs.
+//    places 32 tokens against the whole part in LDS, 64 threads of a column of 16
+//    for each two; two instructions a pair.  Quadratic, but spread over the whole
+//    chip: the 67 M pairs of 8192 tokens take 10 us, 5000 tokens 7 us (4 waves a
+//    workgroup instead of 16: 15 and 13 us, one wave a SIMD hides nothing).  Where
+//    the step's row tiles begin is counted in the same way (bound workgroups), and
+//    the accumulator is cleared meanwhile (zero workgroups).
 //  k_embed_ranks (more than one part): a token's place in its own part, plus for
 //    every earlier part the number of tokens with a row <= its own, for every later
-//    part of those with a smaller row (binary searches).
+//    part of those with a smaller row (binary searches); the bounds likewise.
 // ------------------------------------------------------------------------
-constexpr int PLACE_TOKENS = 16;
+constexpr int PLACE_TOKENS = 32;     // 2 per thread: an LDS read serves two counts
+constexpr int PLACE_NT = 1024, PLACE_WAVES = PLACE_NT / 64, PLACE_STEP = 4 * PLACE_NT / 16;
 
-__global__ void __launch_bounds__(NT) k_embed_place(const EmbedArgs e, int one_part) {
+// bounds: tile[i] = the first place whose row is >= i * rows, for i = 0 .. bounds - 1.
+struct SortArgs {
+  EmbedArgs e;
+  int64_t rows, bounds;
+  ZeroArgs zero;
+  int32_t place_wgs, bound_wgs, parts;
+};
+
+__global__ void __launch_bounds__(PLACE_NT) k_embed_place(const SortArgs a) {
   __shared__ __attribute__((aligned(16))) uint32_t row[EMBED_PART];
-  __shared__ int sums[4][PLACE_TOKENS];
+  __shared__ int sums[PLACE_WAVES][PLACE_TOKENS];
+  const EmbedArgs& e = a.e;
+  const int wg = (int)blockIdx.x - a.place_wgs;                     // < 0: places tokens
+  if (wg >= a.bound_wgs) {
+    zero_rows<FMT_F32>(a.zero, wg - a.bound_wgs, (int64_t)gridDim.x - a.place_wgs - a.bound_wgs, PLACE_NT);
+    return;
+  }
   constexpr int per_part = EMBED_PART / PLACE_TOKENS;
-  const int64_t n0 = (int64_t)(blockIdx.x / per_part) * EMBED_PART;
-  const int i0 = (int)(blockIdx.x % per_part) * PLACE_TOKENS;       // first token, within the part
+  const int64_t n0 = wg < 0 ? (int64_t)(blockIdx.x / per_part) * EMBED_PART : 0;
+  const int i0 = wg < 0 ? (int)(blockIdx.x % per_part) * PLACE_TOKENS : EMBED_PART;   // first token, within the part
   const int n = (int)min((int64_t)EMBED_PART, e.T - n0);
-  if (i0 >= n) return;
-  const int n64 = (n + 63) & ~63;
-  for (int b = threadIdx.x; b < n64; b += 8 * NT) {
+  const int all = (n + PLACE_STEP - 1) & ~(PLACE_STEP - 1);
+  for (int b = threadIdx.x; b < all; b += 8 * PLACE_NT) {
     int64_t id[8];
-    load_ids(e.ids, e.id_bytes, [&](int u) { return n0 + min(b + u * NT, n - 1); }, id);
+    load_ids(e.ids, e.id_bytes, [&](int u) { return n0 + min(b + u * PLACE_NT, n - 1); }, id);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int i = b + u * NT;
-      if (i < n64) row[i] = i < n ? (uint32_t)id_row(id[u], e.V) : 0xFFFFFFFFu;   // past the end: never smaller
+      const int i = b + u * PLACE_NT;
+      if (i < all) row[i] = i < n ? (uint32_t)id_row(id[u], e.V) : 0xFFFFFFFFu;   // past the end: never smaller
     }
   }
   __syncthreads();
-  const int sub = threadIdx.x >> 4, i = i0 + (threadIdx.x & 15);    // 16 subsets of the part by 16 tokens
-  const uint32_t own = i < n ? row[i] : 0u;
-  int count = 0;
+  const int sub = threadIdx.x >> 4;                                 // 64 subsets of the part by 16 pairs of tokens
+  int i[2], count[2] = {0, 0};
+  uint32_t own[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int k = 16 * h + (threadIdx.x & 15);
+    i[h] = i0 + k;
+    own[h] = wg < 0 ? row[min(i[h], n - 1)] : (uint32_t)min(((int64_t)wg * PLACE_TOKENS + k) * a.rows, e.V);
+  }
 #pragma unroll 4
-  for (int j0 = 0; j0 < n64; j0 += 64) {
+  for (int j0 = 0; j0 < all; j0 += PLACE_STEP) {
     const int j = j0 + 4 * sub;
     const u32x4 r = *reinterpret_cast<const u32x4*>(row + j);
-    if (j0 + 64 <= i0 || j0 >= i0 + PLACE_TOKENS) {
+    if (wg >= 0 || j0 + PLACE_STEP <= i0 || j0 >= i0 + PLACE_TOKENS) {
       // all of these come before every token of the workgroup, or all after
-      const uint32_t lim = own + (j0 < i0 ? 1u : 0u);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) count += r[k] < lim ? 1 : 0;
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lim = own[h] + (wg < 0 && j0 < i0 ? 1u : 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) count[h] += r[k] < lim ? 1 : 0;
+      }
     } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) count += r[k] < own + (j + k < i ? 1u : 0u) ? 1 : 0;
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) count[h] += r[k] < own[h] + (j + k < i[h] ? 1u : 0u) ? 1 : 0;
     }
   }
-  count += __shfl_xor(count, 16);
-  count += __shfl_xor(count, 32);
-  if ((threadIdx.x & 63) < PLACE_TOKENS) sums[threadIdx.x >> 6][threadIdx.x & 15] = count;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    count[h] += __shfl_xor(count[h], 16);
+    count[h] += __shfl_xor(count[h], 32);
+    if ((threadIdx.x & 63) < 16) sums[threadIdx.x >> 6][16 * h + (threadIdx.x & 15)] = count[h];
+  }
   __syncthreads();
-  if (threadIdx.x < PLACE_TOKENS && i < n) {
-    const int64_t at = n0 + sums[0][threadIdx.x] + sums[1][threadIdx.x] + sums[2][threadIdx.x] + sums[3][threadIdx.x];
-    if (one_part) {
-      e.key[at] = (int32_t)own;
-      e.perm[at] = i;
-    } else {
-      e.part[at] = ((uint64_t)own << 32) | (uint64_t)(n0 + i);
-    }
+  if (threadIdx.x >= PLACE_TOKENS) return;
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < PLACE_WAVES; ++w) at += sums[w][threadIdx.x];
+  if (wg >= 0) {
+    const int64_t k = (int64_t)wg * PLACE_TOKENS + threadIdx.x;
+    if (k < a.bounds) e.tile[k] = at;
+    return;
+  }
+  const int t = i0 + threadIdx.x;
+  if (t >= n) return;
+  const uint32_t v = row[t];
+  if (a.parts == 1) {
+    e.key[at] = (int32_t)v;
+    e.perm[at] = t;
+  } else {
+    e.part[n0 + at] = ((uint64_t)v << 32) | (uint64_t)(n0 + t);
   }
 }
 
@@ -182,31 +243,47 @@ __device__ __forceinline__ int part_lower(const uint64_t* a, int n, uint64_t r) 
   return lo;
 }
 
-__global__ void __launch_bounds__(NT) k_embed_ranks(const EmbedArgs e) {
+__global__ void __launch_bounds__(NT) k_embed_ranks(const SortArgs a) {
+  const EmbedArgs& e = a.e;
   const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
-  if (i >= e.T) return;
-  const uint64_t x = e.part[i], row = x >> 32;
-  const int64_t own = i / EMBED_PART;
-  int64_t rank = i - own * EMBED_PART;
+  if (i >= e.T + a.bounds) return;
+  const bool token = i < e.T;
+  const uint64_t x = token ? e.part[i] : 0;
+  const uint64_t row = token ? x >> 32 : (uint64_t)min((i - e.T) * a.rows, e.V);
+  const int64_t own = token ? i / EMBED_PART : -1;
+  int64_t rank = token ? i - own * EMBED_PART : 0;
   for (int64_t b = 0, n0 = 0; n0 < e.T; ++b, n0 += EMBED_PART) {
     if (b == own) continue;
     rank += part_lower(e.part + n0, (int)min((int64_t)EMBED_PART, e.T - n0), b < own ? row + 1 : row);
   }
-  e.key[rank] = (int32_t)row;
-  e.perm[rank] = (int32_t)(x & 0xFFFFFFFFu);
+  if (token) {
+    e.key[rank] = (int32_t)row;
+    e.perm[rank] = (int32_t)(x & 0xFFFFFFFFu);
+  } else {
+    e.tile[i - e.T] = (int32_t)rank;
+  }
 }
 
-hipError_t launch_embed_sort(const EmbedArgs& e, hipStream_t st) {
-  if (e.T == 0) return hipSuccess;
-  const int64_t parts = (e.T + EMBED_PART - 1) / EMBED_PART;
-  const int64_t last = e.T - (parts - 1) * EMBED_PART;
-  const unsigned grid =
-      (unsigned)((parts - 1) * (EMBED_PART / PLACE_TOKENS) + (last + PLACE_TOKENS - 1) / PLACE_TOKENS);
-  hipLaunchKernelGGL(k_embed_place, dim3(grid), dim3(NT), 0, st, e, parts == 1 ? 1 : 0);
+// Sort the tokens; bounds > 0: where each `rows` rows begin too; zero.rows > 0: clear those.
+static hipError_t sort_tokens(const EmbedArgs& e, int64_t rows, int64_t bounds, const ZeroArgs& zero, hipStream_t st) {
+  SortArgs a{e, rows, bounds, zero, 0, 0, (int32_t)((e.T + EMBED_PART - 1) / EMBED_PART)};
+  if (e.T > 0) {
+    const int64_t last = e.T - (int64_t)(a.parts - 1) * EMBED_PART;
+    a.place_wgs = (int32_t)((a.parts - 1) * (EMBED_PART / PLACE_TOKENS) + (last + PLACE_TOKENS - 1) / PLACE_TOKENS);
+    if (a.parts == 1) a.bound_wgs = (int32_t)((bounds + PLACE_TOKENS - 1) / PLACE_TOKENS);
+  }
+  const int64_t per = PLACE_NT >> zero.sh, zero_wgs = std::min<int64_t>((zero.rows + per - 1) / per, 1 << 20);
+  const unsigned grid = (unsigned)(a.place_wgs + a.bound_wgs + zero_wgs);
+  if (grid == 0) return hipSuccess;
+  hipLaunchKernelGGL(k_embed_place, dim3(grid), dim3(PLACE_NT), 0, st, a);
   const hipError_t err = hipGetLastError();
-  if (err != hipSuccess || parts == 1) return err;
-  hipLaunchKernelGGL(k_embed_ranks, dim3((unsigned)((e.T + NT - 1) / NT)), dim3(NT), 0, st, e);
+  if (err != hipSuccess || a.parts <= 1) return err;
+  hipLaunchKernelGGL(k_embed_ranks, dim3((unsigned)((e.T + bounds + NT - 1) / NT)), dim3(NT), 0, st, a);
   return hipGetLastError();
+}
+
+hipError_t launch_embed_sort(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t st) {
+  return sort_tokens(e, rows, e.T > 0 ? tiles + 1 : 0, ZeroArgs{nullptr, 0, 0, 0, 0}, st);
 }
 
 // ------------------------------------------------------------------------
@@ -335,15 +412,8 @@ __global__ void __launch_bounds__(NT) k_embed_rows(const EmbedArgs e, float* acc
 
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t st) {
   if (e.V == 0 || e.K == 0) return hipSuccess;
-  if (first) {
-    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)std::min<int64_t>(e.V, 1 << 20)), dim3(NT), 0, st, acc, ldacc,
-                       (int)FMT_F32, e.V, e.K);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  if (e.T == 0) return hipSuccess;
-  const hipError_t err = launch_embed_sort(e, st);
-  if (err != hipSuccess) return err;
+  const hipError_t err = sort_tokens(e, 0, 0, ZeroArgs{acc, ldacc, first ? e.V : 0, e.K, lane_shift(e.K, 4, 10)}, st);
+  if (err != hipSuccess || e.T == 0) return err;
   const int64_t long_units = e.T > ROW_LONG ? (e.T + ROW_LONG - 1) / ROW_LONG * ((e.K + ROW_SEG - 1) / ROW_SEG) : 0;
   const int64_t shorts = (e.T * ((e.K + ROW_COLS - 1) / ROW_COLS) + 3) / 4;
   const int longs = (int)std::min<int64_t>(long_units, 2048);
@@ -358,31 +428,8 @@ hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc
 #undef FORGE_ROWS
 }
 
-// tile[i] = the first place whose row is >= i * rows, for i = 0 .. tiles (the step's
-// row tiles and the end of the last).
-__global__ void __launch_bounds__(NT) k_embed_tiles(const EmbedArgs e, int64_t rows, int64_t tiles) {
-  const int64_t i = (int64_t)blockIdx.x * NT + threadIdx.x;
-  if (i > tiles) return;
-  const int64_t r = min(i * rows, e.V);
-  int64_t lo = 0, n = e.T;
-  while (n > 0) {
-    const int64_t h = n >> 1;
-    const bool less = e.key[lo + h] < r;
-    lo = less ? lo + h + 1 : lo;
-    n = less ? n - h - 1 : h;
-  }
-  e.tile[i] = (int32_t)lo;
-}
-
-hipError_t launch_embed_tiles(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t st) {
-  hipLaunchKernelGGL(k_embed_tiles, dim3((unsigned)(tiles / NT + 1)), dim3(NT), 0, st, e, rows, tiles);
-  return hipGetLastError();
-}
-
 hipError_t launch_embed_step(const KArgs& a, const EmbedArgs& e, int w_fmt, int opt, int m_fmt, int v_fmt,
                              hipStream_t st) {
-  const hipError_t err = launch_embed_sort(e, st);
-  if (err != hipSuccess) return err;
 #define X(O, M, V) \
   if (opt == O && m_fmt == M && v_fmt == V) return combo_embed<O, M, V>(a, e, w_fmt, st);
   FORGE_STATE_LIST(X)
