@@ -59,10 +59,12 @@ class forge_mat(ctypes.Structure):
 
 class forge_state(ctypes.Structure):
     _fields_ = [("q", forge_mat), ("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
+    tensors = ()     # act8(): the tensors behind the addresses
 
 
 class forge_act8(ctypes.Structure):
     _fields_ = [("q", forge_mat), ("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
+    tensors = ()     # act8(): the tensors behind the addresses
 
 
 class forge_hyper(ctypes.Structure):
@@ -495,16 +497,20 @@ def forge_wgrad_unfused(X, dY, W, m, v, h: forge_hyper, step: int, seed: int, dW
 
 def _launch(name, stream, check, fn, tensors, *args):
     """Call fn(*args, stream) on the device of the tensors, which need not be the
-    current one; they must all be on one (structs made from raw pointers say nothing
+    current one; they must all be on one GPU (structs made from raw pointers say nothing
     about theirs).  Without a stream: that device's current one."""
     device = None
     for t in tensors:
+        if isinstance(t, forge_act8):
+            t = t.tensors and t.tensors[0]
         if isinstance(t, torch.Tensor):
             if device is None:
                 device = t.device
+                if device.type != "cuda":
+                    raise ValueError(f"{name}: tensors on {device}, expected a GPU")
             elif t.device != device:
                 raise ValueError(f"{name}: tensors on {device} and {t.device} in one call")
-    if device is None or device.type != "cuda" or device.index == torch.cuda.current_device():
+    if device is None or device.index == torch.cuda.current_device():
         rc = fn(*args, current_stream() if stream is None else stream)
     else:
         with torch.cuda.device(device):
@@ -554,18 +560,18 @@ def _ids(ids):
 
 def forge_act_quantize(X, Q: forge_act8, stream=None, check: bool = True) -> int:
     """Q (codes and power-of-two block scales) = X in 8 bits; Q from act8()."""
-    return _launch("forge_act_quantize", stream, check, lib.forge_act_quantize, (X,), _ref(_as_mat(X)), _ref(Q))
+    return _launch("forge_act_quantize", stream, check, lib.forge_act_quantize, (X, Q), _ref(_as_mat(X)), _ref(Q))
 
 
 def forge_act_dequantize(Q: forge_act8, X, stream=None, check: bool = True) -> int:
     """X (bf16 or float32) = the values Q holds, exactly."""
-    return _launch("forge_act_dequantize", stream, check, lib.forge_act_dequantize, (X,), _ref(Q), _ref(_as_mat(X)))
+    return _launch("forge_act_dequantize", stream, check, lib.forge_act_dequantize, (X, Q), _ref(Q), _ref(_as_mat(X)))
 
 
 def forge_wgrad_step_act8(X: forge_act8, dY, W, m, v, h: forge_hyper, step: int, seed: int, stream=None,
                           check: bool = True) -> int:
     """forge_wgrad_step with X from its 8-bit copy (dY bf16)."""
-    return _launch("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, (dY, W), _ref(X),
+    return _launch("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, (dY, W, X), _ref(X),
                    _ref(_as_mat(dY)), _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed)
 
 
@@ -575,7 +581,7 @@ def forge_wgrad_check_act8(X: forge_act8, dY: forge_mat, W: forge_mat, m, v, h: 
 
 def forge_wgrad_accumulate_act8(X: forge_act8, dY, acc, first: bool, stream=None, check: bool = True) -> int:
     """forge_wgrad_accumulate with X from its 8-bit copy (dY bf16)."""
-    return _launch("forge_wgrad_accumulate_act8", stream, check, lib.forge_wgrad_accumulate_act8, (dY, acc), _ref(X),
+    return _launch("forge_wgrad_accumulate_act8", stream, check, lib.forge_wgrad_accumulate_act8, (dY, acc, X), _ref(X),
                    _ref(_as_mat(dY)), _ref(_as_mat(acc)), 1 if first else 0)
 
 
@@ -587,7 +593,7 @@ def forge_rmsnorm(X, gamma, Y=None, eps: float = 1e-5, R=None, H=None, Q: Option
     [rows], kept for forge_rmsnorm_backward.  Every output but one may be None.
     """
     x = _as_mat(X)
-    return _launch("forge_rmsnorm", stream, check, lib.forge_rmsnorm, (X, gamma, Y, R, H, rstd), _ref(x),
+    return _launch("forge_rmsnorm", stream, check, lib.forge_rmsnorm, (X, gamma, Y, R, H, rstd, Q), _ref(x),
                    _ref(_as_mat(R)), _ref(_row_mat(gamma)), eps, _ref(_as_mat(H)), _ref(_as_mat(Y)), _ref(Q),
                    _floats(rstd, x.rows, "rstd"))
 

@@ -454,7 +454,8 @@ forge_status forge_wgrad_accumulate_act8(const forge_act8* X, const forge_mat* d
  * rstd  : rows floats (s, which the backward pass reads), or NULL.
  * eps   : finite, >= 0.  rows, cols < 2^31.
  * At least one of H, Y, Q, rstd must be given (else E_NULL).  No rows or no
- * columns: a no-op.
+ * columns: a no-op.  The mean is taken in fp32: a row whose sum of squares passes
+ * its range (|H| from about 1e19 on) has s = 0.
  * Errors: FORGE_E_NULL, E_SHAPE, E_DTYPE, E_ALIGN, E_HYPER (eps), E_ALIAS
  * (nothing enqueued) or E_HIP.
  */

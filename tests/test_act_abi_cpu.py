@@ -249,4 +249,22 @@ def test_binding_checks_its_tensors():
     with pytest.raises(ValueError):   # two devices in one call
         F.forge_rmsnorm(x, g.to("meta"), x.clone(), stream=0)
     with pytest.raises(F.ForgeError):
-        F.forge_embed(torch.zeros(4, dtype=torch.int64), torch.zeros(4, 100), torch.zeros(3, 100), stream=0)
+        F.forge_act_quantize(mat(0, 3, 100), act(1, 4, 100), stream=0)
+
+
+def test_binding_refuses_host_tensors():
+    """An address of host memory would fault in a kernel: tensors that are not on a GPU are refused before the call."""
+    x, g, ids = torch.zeros(4, 64), torch.ones(64), torch.zeros(4, dtype=torch.int64)
+    q = F.act8(torch.zeros((4, 64), dtype=torch.int8), torch.zeros((4, 1), dtype=torch.uint8), 64)
+    st, h = F.state(torch.zeros(4, 64)), F.hyper("sgdm")
+    ws = torch.zeros(F.forge_embed_workspace_bytes(4, 4), dtype=torch.uint8)
+    raw = mat(0, 4, 64, F.FORGE_F32)
+    for call in (lambda: F.forge_act_quantize(x, q), lambda: F.forge_act_dequantize(q, raw),
+                 lambda: F.forge_wgrad_step_act8(q, raw, raw, st, None, h, 1, 0),
+                 lambda: F.forge_wgrad_accumulate_act8(q, raw, raw, True), lambda: F.forge_rmsnorm(x, g, torch.empty_like(x)),
+                 lambda: F.forge_rmsnorm(raw, mat(1, 1, 64), Q=q), lambda: F.forge_embed(ids, raw, raw),
+                 lambda: F.forge_rmsnorm_backward(x, x, g, torch.ones(4), torch.empty_like(x)),
+                 lambda: F.forge_embed_accumulate(ids, raw, raw, True, workspace=ws),
+                 lambda: F.forge_embed_step(ids, raw, raw, st, None, h, 1, 0, workspace=ws)):
+        with pytest.raises(ValueError, match="expected a GPU"):
+            call()
