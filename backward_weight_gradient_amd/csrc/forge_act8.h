@@ -12,6 +12,16 @@ typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(1)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
 
+// Row and column of a workgroup's tile, 8 rows of tiles at a time, each row on one XCD
+// (workgroups go to the 8 XCDs in turn): neighbours in a row share the lines at their
+// seam in that XCD's cache.  The rows left over follow in plain order.
+__device__ __forceinline__ void tile_by_xcd(int rows, int cols, int& ti, int& tj) {
+  const int b = (int)blockIdx.x, g = b / (8 * cols);
+  const bool whole = 8 * g + 8 <= rows;
+  ti = whole ? 8 * g + (b & 7) : b / cols;
+  tj = whole ? (b - 8 * g * cols) >> 3 : b - ti * cols;
+}
+
 constexpr int ACT8_EMIN = -120;           // smallest exponent: the smallest E4M3 step, 2^-9, stays exact in bf16 (2^-133)
 constexpr uint32_t ACT8_NAN = 255;        // scale byte of a block that held an infinity or a NaN
 

@@ -98,14 +98,7 @@ __global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const Embed
   __shared__ float red[3 * TILE];
   constexpr int MODE = FAST || ANY ? ROW_BIG : ROW_ANY;
   int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
-  if (ANY) {          // 8 rows of tiles at a time, one to an XCD (workgroups go to the 8 in turn)
-    const int rows8 = (int)gridDim.x / (8 * a.tiles_k) * 8, b = (int)blockIdx.x;
-    if (b < rows8 * a.tiles_k) {
-      const int g = b / (8 * a.tiles_k);
-      ti = 8 * g + (b & 7);
-      tj = (b - 8 * g * a.tiles_k) >> 3;
-    }
-  }
+  if (ANY) tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
   const int row0 = ti * ROWS, col0 = tj * TILE;
   Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, ROWS> epi;
   epi.tid = threadIdx.x;

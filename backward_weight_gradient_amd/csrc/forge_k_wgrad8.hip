@@ -44,7 +44,8 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8_dma(const KArgs8 a) {
 
 __global__ void __launch_bounds__(2 * NT, 1) k_gemm_act8_split(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
-  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  int ti, tj;
+  tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
   f32x16 acc[2][4];
   if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);
   else Act8Split::run<FMT_E4M3>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);

@@ -672,7 +672,8 @@ struct Act8Split {
 template <int OPT, int WF, int MF, int VF>
 __global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_split(const KArgs8 a) {
   __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
-  const int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
+  int ti, tj;
+  tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
   const int row0 = ti * SPLIT_ROWS, col0 = tj * TILE;
   f32x16 acc[2][4];
   if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, row0, col0, acc);
