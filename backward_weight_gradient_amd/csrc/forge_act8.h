@@ -302,7 +302,7 @@ __device__ __forceinline__ void act8_store8(const Act8& q, int64_t r, int64_t c,
 
 // s += the rows at(0) .. at(mine - 1) of an array of type FMT at column c, in order.
 // at(i) is the address of a row's element 0, valid for every i (callers clamp it);
-// count: the largest `mine` of the wave.  8 or 4 rows are in flight at a time, those
+// count: the largest `mine` of the wave.  B or B / 2 rows are in flight at a time, those
 // past the lane's own count read and left out, so no load waits for another.
 template <int MODE, int FMT, int B, class AT>
 __device__ __forceinline__ void sum_rows_batch(AT&& at, int m, int mine, int64_t c, int64_t K, float (&s)[8]) {
@@ -317,11 +317,11 @@ __device__ __forceinline__ void sum_rows_batch(AT&& at, int m, int mine, int64_t
     for (int k = 0; k < 8; ++k) s[k] = m + u < mine ? s[k] + x[k] : s[k];
   }
 }
-template <int MODE, int FMT, class AT>
+template <int MODE, int FMT, int B = 8, class AT>
 __device__ __forceinline__ void sum_rows(AT&& at, int count, int mine, int64_t c, int64_t K, float (&s)[8]) {
   int m = 0;
-  for (; count - m > 4; m += 8) sum_rows_batch<MODE, FMT, 8>(at, m, mine, c, K, s);
-  if (count - m > 1) sum_rows_batch<MODE, FMT, 4>(at, m, mine, c, K, s);
+  for (; count - m > B / 2; m += B) sum_rows_batch<MODE, FMT, B>(at, m, mine, c, K, s);
+  if (count - m > 1) sum_rows_batch<MODE, FMT, B / 2>(at, m, mine, c, K, s);
   else if (count - m == 1) sum_rows_batch<MODE, FMT, 1>(at, m, mine, c, K, s);
 }
 

@@ -93,7 +93,7 @@ forge_status check_embed_grad(const void* ids, int32_t id_bytes, int64_t T, cons
   if (!dY) return FORGE_E_NULL;
   forge_status st = check_ids(ids, id_bytes, T);
   if (st != FORGE_OK) return st;
-  if (V < 0 || K < 0 || V >= kMax31 - 1 || K >= kMax31) return FORGE_E_SHAPE;
+  if (V < 0 || K < 0 || V >= kMax31 - 1 || K >= kMax31 || T >= EMBED_MAX_TOKENS) return FORGE_E_SHAPE;
   if ((st = check_float_mat(dY, T, K)) != FORGE_OK) return st;
   if (!std::isfinite((float)scale)) return FORGE_E_HYPER;
   const int64_t need = V > 0 && K > 0 ? forge_embed_workspace_bytes(T, V) : 0;
@@ -109,7 +109,7 @@ forge_status check_embed_grad(const void* ids, int32_t id_bytes, int64_t T, cons
   char* p = static_cast<char*>(ws);
   e.key = reinterpret_cast<int32_t*>(p);    p += round16(4 * T);
   e.perm = reinterpret_cast<int32_t*>(p);   p += round16(4 * T);
-  e.tile = reinterpret_cast<int32_t*>(p);   p += round16(4 * (V / EMBED_MIN_ROWS + 2));
+  e.tile = reinterpret_cast<int32_t*>(p);   p += round16(4 * (V / EMBED_ROWS + 2));
   e.part = reinterpret_cast<uint64_t*>(p);
   return FORGE_OK;
 }
@@ -285,8 +285,8 @@ forge_status forge_embed(const void* ids, int32_t id_bytes, int64_t T, const for
 }
 
 int64_t forge_embed_workspace_bytes(int64_t T, int64_t V) {
-  if (T < 0 || V <= 0 || T >= kMax31 || V >= kMax31 - 1) return 0;
-  return 2 * round16(4 * T) + round16(4 * (V / EMBED_MIN_ROWS + 2)) + (T > EMBED_PART ? 8 * T : 0);
+  if (T < 0 || V <= 0 || T >= EMBED_MAX_TOKENS || V >= kMax31 - 1) return 0;
+  return 2 * round16(4 * T) + round16(4 * (V / EMBED_ROWS + 2)) + (T > EMBED_PART ? 8 * T : 0);
 }
 
 forge_status forge_embed_accumulate(const void* ids, int32_t id_bytes, int64_t T, const forge_mat* dY, double scale,
@@ -322,6 +322,7 @@ forge_status forge_embed_step(const void* ids, int32_t id_bytes, int64_t T, cons
   layer_ranges(&none_x, &none_y, W, m, v, pl, outs, ins);
   for (const Range& r : outs) u.add(r, true);
   if ((st = u.check()) != FORGE_OK) return st;
+  if ((V + EMBED_ROWS - 1) / EMBED_ROWS * ((K + 127) / 128) >= EMBED_MAX_TILES) return FORGE_E_SHAPE;
   if (pl.empty) return FORGE_OK;
   const KArgs a = make_args(&none_x, &none_y, W, m, v, h, step, seed, pl);
   return hip_status(launch_embed_step(a, e, pl.w_fmt, h->opt, pl.m_fmt, pl.v_fmt, (hipStream_t)stream));

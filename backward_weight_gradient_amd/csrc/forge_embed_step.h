@@ -6,12 +6,12 @@
 
 namespace forge {
 
-// G tile (ROWS rows of W from row0, 128 columns from col0) into LDS:
+// G tile (EMBED_ROWS rows of W from row0, 128 columns from col0) into LDS:
 //   sG[r * GP + c] = scale * sum over the tokens of row row0 + r of dY[token][col0 + c].
 // first, last: the tile's places among the sorted tokens.  16 lanes of 8 columns per
 // token.  A row of up to LONG_ROW tokens belongs to one wave, 4 tokens at a time; a
 // longer one to the whole workgroup, 16 at a time.  Sums over a slot's tokens in
-// order, then over the slots in a fixed order.  rng: 2 ROWS ints, red: 3 x 128 floats.
+// order, then over the slots in a fixed order.  rng: 2 EMBED_ROWS ints, red: 3 x 128 floats.
 constexpr int LONG_ROW = 32;
 
 // Tokens slot, slot + step, .. of first .. last - 1 of the sorted ones, and then the sum
@@ -25,7 +25,8 @@ __device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int
   const auto at = [&](int i) {
     return static_cast<const char*>(e.dY) + (int64_t)e.perm[min(first + slot + i * step, last - 1)] * e.lddy * ds;
   };
-  sum_rows<MODE, DF>(at, (last - first + step - 1) / step, (last - first - slot + step - 1) / step, c, e.K, s);
+  // (half as many fp32 rows at a time: the kernel keeps to 128 registers)
+  sum_rows<MODE, DF, DF == FMT_F32 ? 4 : 8>(at, (last - first + step - 1) / step, (last - first - slot + step - 1) / step, c, e.K, s);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     s[k] += __shfl_xor(s[k], 16);
@@ -33,18 +34,18 @@ __device__ __forceinline__ void gather_tokens(const EmbedArgs& e, int first, int
   }
 }
 
-template <int MODE, int DF, int ROWS>
+template <int MODE, int DF>
 __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* rng, float* red, int row0, int col0, int first,
                                            int last) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int cl = 8 * (lane & 15);
   const int64_t c = (int64_t)col0 + cl;
-  for (int i = tid; i < ROWS * GP / 4; i += NT) reinterpret_cast<f32x4*>(sG)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = tid; i < EMBED_ROWS * GP / 4; i += NT) reinterpret_cast<f32x4*>(sG)[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (first >= last) {     // (the same for the whole workgroup)
     __syncthreads();
     return;
   }
-  for (int i = tid; i < 2 * ROWS; i += NT) rng[i] = 0;
+  for (int i = tid; i < 2 * EMBED_ROWS; i += NT) rng[i] = 0;
   __syncthreads();
   for (int p = first + tid; p < last; p += NT) {
     const int k = e.key[p];
@@ -52,91 +53,86 @@ __device__ __forceinline__ void embed_tile(const EmbedArgs& e, float* sG, int* r
     if (p + 1 == last || e.key[p + 1] != k) rng[2 * (k - row0) + 1] = p + 1;
   }
   __syncthreads();
+  const int r = lane;
+  const int n = r < EMBED_ROWS ? rng[2 * r + 1] - rng[2 * r] : 0;
+  // rows of this wave (r % 4 == wave) with few tokens, then the long rows with all waves
+  uint64_t mine = __ballot(n > 0 && n <= LONG_ROW && (r & 3) == wave), all = __ballot(n > LONG_ROW);
+  while (mine) {
+    const int k = __builtin_ctzll(mine);
+    mine &= mine - 1;
+    float s[8];
+    gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], lane >> 4, 4, c, s);
+    if (lane < 16) {
 #pragma unroll
-  for (int base = 0; base < ROWS; base += 64) {
-    const int r = base + lane;
-    const int n = r < ROWS ? rng[2 * r + 1] - rng[2 * r] : 0;
-    // rows of this wave (r % 4 == wave) with few tokens, then the long rows with all waves
-    uint64_t mine = __ballot(n > 0 && n <= LONG_ROW && (r & 3) == wave), all = __ballot(n > LONG_ROW);
-    while (mine) {
-      const int k = base + __builtin_ctzll(mine);
-      mine &= mine - 1;
-      float s[8];
-      gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], lane >> 4, 4, c, s);
-      if (lane < 16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sG[k * GP + cl + i] = s[i] * e.scale;
-      }
+      for (int i = 0; i < 8; ++i) sG[k * GP + cl + i] = s[i] * e.scale;
     }
-    while (all) {   // the same rows in every wave
-      const int k = base + __builtin_ctzll(all);
-      all &= all - 1;
-      float s[8];
-      gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], tid >> 4, 16, c, s);
-      if (wave > 0 && lane < 16) {
+  }
+  while (all) {   // the same rows in every wave
+    const int k = __builtin_ctzll(all);
+    all &= all - 1;
+    float s[8];
+    gather_tokens<MODE, DF>(e, rng[2 * k], rng[2 * k + 1], tid >> 4, 16, c, s);
+    if (wave > 0 && lane < 16) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) red[(wave - 1) * TILE + cl + i] = s[i];
-      }
-      __syncthreads();
-      if (wave == 0 && lane < 16) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          sG[k * GP + cl + i] =
-              (((s[i] + red[cl + i]) + red[TILE + cl + i]) + red[2 * TILE + cl + i]) * e.scale;
-      }
-      __syncthreads();
+      for (int i = 0; i < 8; ++i) red[(wave - 1) * TILE + cl + i] = s[i];
     }
+    __syncthreads();
+    if (wave == 0 && lane < 16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        sG[k * GP + cl + i] =
+            (((s[i] + red[cl + i]) + red[TILE + cl + i]) + red[2 * TILE + cl + i]) * e.scale;
+    }
+    __syncthreads();
   }
   __syncthreads();
 }
 
 // FAST, ANY: rows of at least 8 elements, ANY of any alignment.
-template <int ROWS, bool FAST, bool ANY, int OPT, int WF, int MF, int VF>
-__global__ void __launch_bounds__(NT, 2) k_embed_step(const KArgs a, const EmbedArgs e) {
-  __shared__ __attribute__((aligned(16))) float sG[ROWS * GP];
-  __shared__ int rng[2 * ROWS];
+template <bool FAST, bool ANY, int OPT, int WF, int MF, int VF>
+__global__ void __launch_bounds__(NT, 4) k_embed_step(const KArgs a, const EmbedArgs e) {
+  __shared__ __attribute__((aligned(16))) float sG[EMBED_ROWS * GP];
+  __shared__ int rng[2 * EMBED_ROWS];
   __shared__ float red[3 * TILE];
   constexpr int MODE = FAST || ANY ? ROW_BIG : ROW_ANY;
   int ti = (int)blockIdx.x / a.tiles_k, tj = (int)blockIdx.x - ti * a.tiles_k;
   if (ANY) tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
-  const int row0 = ti * ROWS, col0 = tj * TILE;
-  Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, ROWS> epi;
+  const int row0 = ti * EMBED_ROWS, col0 = tj * TILE;
+  Epilogue<Step<OPT, WF, MF, VF, FAST, 0, ANY>, FMT_NONE, FAST, 4, NT, false, false, EMBED_ROWS> epi;
   epi.tid = threadIdx.x;
   epi.prefetch(a, row0, col0);
   const int first = e.T ? e.tile[ti] : 0, last = e.T ? e.tile[ti + 1] : 0;
-  if (e.dy_fmt == FMT_F32) embed_tile<MODE, FMT_F32, ROWS>(e, sG, rng, red, row0, col0, first, last);
-  else embed_tile<MODE, FMT_BF16, ROWS>(e, sG, rng, red, row0, col0, first, last);
+  if (e.dy_fmt == FMT_F32) embed_tile<MODE, FMT_F32>(e, sG, rng, red, row0, col0, first, last);
+  else embed_tile<MODE, FMT_BF16>(e, sG, rng, red, row0, col0, first, last);
   epi.run_prefetched(a, sG, row0, col0);
 }
 
 // FAST: rows of whole 128-byte lines, whose accesses bypass the caches and whose
 // tiles go out row of tiles by row.  Other rows share lines at the tiles' seams, and
 // streaming parts of lines through different XCDs costs far more than the lines
-// themselves: 37929 x 2984 bf16 629 us so, 337 us with cached accesses and neighbouring
-// tiles on one XCD (46421 x 1459, fp32 state: 530 and 316).
+// themselves: with tiles of 128 rows 37929 x 2984 took 629 us so, 337 with cached
+// accesses and neighbouring tiles on one XCD (46421 x 1459 530 and 316).
 //
-// Tiles of 128 rows, or of 16 where those would be fewer than two per CU: then a
-// step is bound by the gathering of each tile's tokens, not by HBM.
+// Tiles of 16 rows, four workgroups to a CU: small ones hide each other's gathering.
+// With AdamW, bf16 W and fp32 moments 8192 tokens of 128256 x 4096 take 1773 us (10.6 GB,
+// 6.0 TB/s: bound by HBM), 1837 with tiles of 128 rows; 8192 of 32000 x 4096 458 and 502
+// (two workgroups to a CU: 500); 4096 of 1000 x 1024, bound by latency, 17 and 44; the
+// unaligned 46421 x 1459 280 and 313, 37929 x 2985 316 and 352.
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
   const bool fast = a.vec_state && a.K % 64 == 0 && a.ldw % 64 == 0 && a.ldm % 64 == 0 && a.ldv % 64 == 0;
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
-  const int64_t rows = (int64_t)a.tiles_n * a.tiles_k >= 512 && a.K >= 8 ? TILE : EMBED_MIN_ROWS;
-  const int64_t tiles = (a.N + rows - 1) / rows;
-  const hipError_t err = launch_embed_sort(e, rows, tiles, st);
+  const int64_t tiles = (a.N + EMBED_ROWS - 1) / EMBED_ROWS;
+  const hipError_t err = launch_embed_sort(e, tiles, st);
   if (err != hipSuccess) return err;
   const dim3 grid((unsigned)(tiles * a.tiles_k));
-#define FORGE_EMBED(ROWS, FA, ANY)                                                                                          \
-  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<ROWS, FA, ANY, O, FMT_BF16, M, V>), grid, dim3(NT), 0, st, a, e); \
-  else hipLaunchKernelGGL((k_embed_step<ROWS, FA, ANY, O, FMT_F32, M, V>), grid, dim3(NT), 0, st, a, e);                    \
+#define FORGE_EMBED(FA, ANY)                                                                                          \
+  if (w_fmt == FMT_BF16) hipLaunchKernelGGL((k_embed_step<FA, ANY, O, FMT_BF16, M, V>), grid, dim3(NT), 0, st, a, e); \
+  else hipLaunchKernelGGL((k_embed_step<FA, ANY, O, FMT_F32, M, V>), grid, dim3(NT), 0, st, a, e);                    \
   return hipGetLastError();
-  if (rows == TILE) {
-    if (fast) { FORGE_EMBED(TILE, true, false) }
-    FORGE_EMBED(TILE, false, true)
-  }
-  if (fast) { FORGE_EMBED(EMBED_MIN_ROWS, true, false) }
-  if (a.K >= 8) { FORGE_EMBED(EMBED_MIN_ROWS, false, true) }
-  FORGE_EMBED(EMBED_MIN_ROWS, false, false)
+  if (fast) { FORGE_EMBED(true, false) }
+  if (a.K >= 8) { FORGE_EMBED(false, true) }
+  FORGE_EMBED(false, false)
 #undef FORGE_EMBED
 }
 #define FORGE_INSTANTIATE_EMBED(O, M, V) \

@@ -345,7 +345,8 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t stream);
 // forge_k_embed.hip.  Tokens sorted by id: key[i] (the row), perm[i] (the token), i < T.
 // Padding tokens have key V and so come last.
 constexpr int EMBED_PART = 8192;   // tokens sorted together in LDS
-constexpr int EMBED_MIN_ROWS = 16; // rows of the step's smaller tiles
+constexpr int64_t EMBED_MAX_TOKENS = 1ll << 27, EMBED_MAX_TILES = 1ll << 24;   // a launch has fewer than 2^32 threads
+constexpr int EMBED_ROWS = 16;     // rows of the step's tiles
 struct EmbedArgs {
   const void* ids; int32_t id_bytes;
   int64_t T, V, K;
@@ -357,8 +358,8 @@ struct EmbedArgs {
 };
 hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W, int64_t ldw, int w_fmt, int64_t V,
                         int64_t K, float scale, void* Y, int64_t ldy, int y_fmt, hipStream_t stream);
-// The tokens sorted by id, and where each tile of `rows` rows begins and the last ends.
-hipError_t launch_embed_sort(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t stream);
+// The tokens sorted by id, and where each of the step's tiles begins and the last ends.
+hipError_t launch_embed_sort(const EmbedArgs& e, int64_t tiles, hipStream_t stream);
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t stream);
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st);

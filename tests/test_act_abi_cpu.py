@@ -206,6 +206,7 @@ def test_embed_gradient_refusals(name):
     assert f(width=3) == F.FORGE_E_SHAPE and f(T=9) == F.FORGE_E_SHAPE
     assert f(bytes=F.forge_embed_workspace_bytes(10, 50) - 1) == F.FORGE_E_SHAPE
     assert f(dY=mat(1, 10, 127)) == F.FORGE_E_SHAPE
+    assert f(T=2 ** 27, dY=mat(1, 2 ** 27, 128), bytes=1 << 34) == F.FORGE_E_SHAPE
     assert f(dY=mat(1, 10, 128, F.FORGE_S8)) == F.FORGE_E_DTYPE
     assert f(ws=addr(7) + 8) == F.FORGE_E_ALIGN and f(ids=addr(0) + 2) == F.FORGE_E_ALIGN
     assert f(scale=float("inf")) == F.FORGE_E_HYPER
@@ -216,6 +217,10 @@ def test_embed_gradient_refusals(name):
     else:
         assert f(W=None) == F.FORGE_E_NULL and f(m=None) == F.FORGE_E_NULL and f(h=None) == F.FORGE_E_NULL
         assert f(step=0) == F.FORGE_E_STEP
+        V = 2 ** 28 - 15     # ceil(V / 16) = 2^24 tiles: one too many
+        big = lambda i, dt=F.FORGE_BF16: mat(i, V, 8, dt)
+        assert f(dY=mat(1, 10, 8), W=big(2), m=F.forge_state(big(3), None, 0), v=F.forge_state(big(4), None, 0),
+                 bytes=1 << 34) == F.FORGE_E_SHAPE
         assert f(W=mat(2, 50, 128, F.FORGE_E4M3)) == F.FORGE_E_DTYPE
         assert f(m=F.forge_state(mat(3, 50, 127, F.FORGE_F32), None, 0)) == F.FORGE_E_SHAPE
         assert f(h=F.hyper("lion")) == F.FORGE_E_UNSUPPORTED
@@ -224,7 +229,7 @@ def test_embed_gradient_refusals(name):
 
 def test_embed_workspace_bytes():
     b = F.forge_embed_workspace_bytes
-    assert b(10, 0) == 0 and b(-1, 5) == 0 and b(2 ** 31, 5) == 0
+    assert b(10, 0) == 0 and b(-1, 5) == 0 and b(2 ** 27, 5) == 0
     assert b(0, 5) > 0 and b(1000, 5) > b(10, 5) and b(10, 128256) > b(10, 5)
 
 
