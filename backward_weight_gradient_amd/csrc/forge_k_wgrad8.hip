@@ -42,16 +42,18 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8_dma(const KArgs8 a) {
   store_g<TILE, NT>(a, sG, ti * TILE, tj * TILE);
 }
 
-__global__ void __launch_bounds__(2 * NT, 1) k_gemm_act8_split(const KArgs8 a) {
-  __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
+template <int ROWS, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES, 1) k_gemm_act8_split(const KArgs8 a) {
+  using M = Act8Split<ROWS, WAVES>;
+  __shared__ __attribute__((aligned(16))) char lds[M::LDS];
   int ti, tj;
   tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
-  f32x16 acc[2][4];
-  if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);
-  else Act8Split::run<FMT_E4M3>(a, lds, ti * SPLIT_ROWS, tj * TILE, acc);
+  f32x16 acc[M::BI][4];
+  if (a.x_fmt == FMT_S8) M::template run<FMT_S8>(a, lds, ti * ROWS, tj * TILE, acc);
+  else M::template run<FMT_E4M3>(a, lds, ti * ROWS, tj * TILE, acc);
   float* sG = reinterpret_cast<float*>(lds);
-  Act8Split::join(sG, acc);
-  store_g<SPLIT_ROWS, 2 * NT>(a, sG, ti * SPLIT_ROWS, tj * TILE);
+  M::join(sG, acc);
+  store_g<ROWS, 64 * WAVES>(a, sG, ti * ROWS, tj * TILE);
 }
 
 __global__ void __launch_bounds__(NT, 2) k_gemm_act8_tiny(const KArgs8 a) {
@@ -64,7 +66,9 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8_tiny(const KArgs8 a) {
 
 // The same choice as for the step (the accumulator's rows may be of any alignment).
 hipError_t launch_gemm_act8(const KArgs8& a, hipStream_t st) {
-  if (act8_split(a, a.x_dma)) hipLaunchKernelGGL(k_gemm_act8_split, split_grid(a), dim3(2 * NT), 0, st, a);
+  if (act8_split(a, a.x_dma) && act8_few(a))
+    hipLaunchKernelGGL((k_gemm_act8_split<32, 16>), split_grid<32>(a), dim3(1024), 0, st, a);
+  else if (act8_split(a, a.x_dma)) hipLaunchKernelGGL((k_gemm_act8_split<64, 8>), split_grid<64>(a), dim3(512), 0, st, a);
   else if (a.x_dma && a.x_fmt == FMT_S8) hipLaunchKernelGGL((k_gemm_act8_dma<FMT_S8>), tile_grid(a), dim3(NT), 0, st, a);
   else if (a.x_dma) hipLaunchKernelGGL((k_gemm_act8_dma<FMT_E4M3>), tile_grid(a), dim3(NT), 0, st, a);
   else hipLaunchKernelGGL(k_gemm_act8_tiny, tile_grid(a), dim3(NT), 0, st, a);

@@ -517,19 +517,14 @@ __global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_wide(const KArgs8 a) {
 
 // ------------------------------------------------------------------------
 // Few tiles, or rows the ring does not take (N >= 8, K >= 16): the token axis split
-// over the 8 waves of a workgroup.  A tile is 64
-// rows x 128 columns; wave w takes the 32-token chunks w, w + 8, .. alone, with a
-// slab of LDS of its own (so its loop has no barrier), and the 8 sums are added in
-// a fixed order at the end.  Any alignment: rows are loaded into registers a chunk
-// ahead, the vector that a row ends in shifted into place.
-// LDS: 8 slabs of 12 KiB (dY 32 x 64, X 32 x 128, bf16), then 4 G tiles over them.
+// over the WAVES waves of a workgroup.  A tile is ROWS rows x 128 columns; wave w takes
+// the 32-token chunks w, w + WAVES, .. alone, with a slab of LDS of its own (so its loop
+// has no barrier), and the sums are added in a fixed order at the end.  Any alignment:
+// rows are loaded into registers a chunk ahead, the vector that a row ends in shifted
+// into place.  Bound by the latency of a wave's chunk: 0.6 us with 64 rows and 8 waves.
+// LDS: WAVES slabs of 12 or 10 KiB (dY 32 x ROWS, X 32 x 128, bf16), then WAVES / 2 G
+// tiles over them.
 // ------------------------------------------------------------------------
-constexpr int SPLIT_ROWS = 64, SPLIT_WAVES = 8;
-constexpr int SPLIT_DY = 32 * SPLIT_ROWS * 2, SPLIT_SLAB = SPLIT_DY + 32 * TILE * 2;
-constexpr int SPLIT_G = SPLIT_ROWS * GP;                     // floats of one G tile
-constexpr int LDS_SPLIT = 4 * SPLIT_G * 4;
-static_assert(SPLIT_WAVES * SPLIT_SLAB <= LDS_SPLIT && LDS_SPLIT <= 160 * 1024, "LDS budget");
-
 // 16 codes at column c of a row of K >= 16: the load of those at min(c, K - 16), and
 // what moves them into place.
 __device__ __forceinline__ u32x4 codes_raw16(const uint8_t* p, int64_t c, int64_t K) {
@@ -543,11 +538,21 @@ __device__ __forceinline__ u32x4 codes_shift16(u32x4 w, int s) {   // down by s 
                __builtin_amdgcn_alignbyte(w[3], w[2], s & 3), w[3] >> (8 * (s & 3))};
 }
 
+template <int ROWS, int WAVES>
 struct Act8Split {
-  // byte offset of (token, feature) in the dY half of a slab: 128-byte rows, every
-  // other pair of rows shifted by 64 bytes, so that the 4 rows of a transposing read
+  static constexpr int BI = ROWS / 32;                      // 32-row blocks of the tile
+  static constexpr int DY = 32 * ROWS * 2, SLAB = DY + 32 * TILE * 2;
+  static constexpr int G = ROWS * GP;                       // floats of one G tile
+  static constexpr int LDS = WAVES * SLAB > WAVES / 2 * G * 4 ? WAVES * SLAB : WAVES / 2 * G * 4;
+  static_assert(LDS <= 160 * 1024, "LDS budget");
+  static constexpr int YL = ROWS / 8, NY = YL / 2;          // lanes per token of dY, and its loads per chunk
+
+  // byte offset of (token, feature) in the dY half of a slab: where rows take 128 bytes,
+  // every other pair of them shifted by 64, so that the 4 rows of a transposing read
   // lie in different banks (X's rows: MainBF16::off)
-  __device__ __forceinline__ static int off_dy(int t, int f) { return t * (SPLIT_ROWS * 2) + ((f * 2) ^ ((t & 2) << 5)); }
+  __device__ __forceinline__ static int off_dy(int t, int f) {
+    return t * (ROWS * 2) + ((f * 2) ^ (ROWS == 64 ? (t & 2) << 5 : 0));
+  }
 
   __device__ __forceinline__ static bf16x8 frag(const char* lo, int hi) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -558,27 +563,31 @@ struct Act8Split {
   }
 
   template <int XF>
-  __device__ __forceinline__ static void run(const KArgs8& a, char* lds, int row0, int col0, f32x16 (&acc)[2][4]) {
+  __device__ __forceinline__ static void run(const KArgs8& a, char* lds, int row0, int col0, f32x16 (&acc)[BI][4]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    char* slab = lds + wave * SPLIT_SLAB;
+    char* slab = lds + wave * SLAB;
 #pragma unroll
-    for (int bi = 0; bi < 2; ++bi)
+    for (int bi = 0; bi < BI; ++bi)
 #pragma unroll
       for (int bj = 0; bj < 4; ++bj)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
     const int nk = (a.BT + 31) / 32;
-    const int t0 = lane >> 3;                      // tokens t0 + 8 r of a chunk
-    const int64_t cy = row0 + 8 * (lane & 7), cx = col0 + 16 * (lane & 7);
+    const int t0 = lane >> 3, ty = lane / YL;      // X: tokens t0 + 8 r of a chunk; dY: ty + 64 / YL r
+    const int64_t cy = row0 + 8 * (lane & (YL - 1)), cx = col0 + 16 * (lane & 7);
     const int64_t sx = min(cx, (int64_t)a.K - 1) >> a.x8.sh;
-    Raw8<FMT_BF16> ry[4];
+    Raw8<FMT_BF16> ry[NY];
     u32x4 rx[4];
     uint32_t rs[4];
     const auto request = [&](int kc) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t tok = min((int64_t)kc * 32 + t0 + 8 * r, (int64_t)a.BT - 1);   // past the end: read again, cleared below
+      for (int r = 0; r < NY; ++r) {
+        const int64_t tok = min((int64_t)kc * 32 + ty + 64 / YL * r, (int64_t)a.BT - 1);   // past the end: read again, cleared below
         ry[r] = row_raw8<FMT_BF16, ROW_BIG>(static_cast<const uint16_t*>(a.dY) + tok * a.lddy, cy, a.N);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int64_t tok = min((int64_t)kc * 32 + t0 + 8 * r, (int64_t)a.BT - 1);
         rx[r] = codes_raw16(a.x8.codes + tok * a.x8.ld, cx, a.K);
         rs[r] = (uint32_t)a.x8.scale[tok * a.x8.nb + sx];
       }
@@ -587,47 +596,51 @@ struct Act8Split {
     if (wave < nk) request(wave);
     // Only the vectors that a row ends in need moving; one wholly past the end holds
     // other columns' values, which reach nothing but elements of G that are not stored.
-    const bool move = (row0 + SPLIT_ROWS > a.N && (a.N & 7)) || (col0 + TILE > a.K && (a.K & 15));
+    const bool move = (row0 + ROWS > a.N && (a.N & 7)) || (col0 + TILE > a.K && (a.K & 15));
     const int ey = (int)min((int64_t)7, cy - min(cy, (int64_t)a.N - 8)), ex = (int)min((int64_t)15, cx - min(cx, (int64_t)a.K - 16));
-    for (int kc = wave; kc < nk; kc += SPLIT_WAVES) {
+    for (int kc = wave; kc < nk; kc += WAVES) {
       if (move) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          ry[r] = raw_shift8<FMT_BF16>(ry[r], ey);
-          rx[r] = codes_shift16(rx[r], ex);
-        }
+        for (int r = 0; r < NY; ++r) ry[r] = raw_shift8<FMT_BF16>(ry[r], ey);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) rx[r] = codes_shift16(rx[r], ex);
       }
       if (kc * 32 + 32 > a.BT) {   // tokens past the end
 #pragma unroll
+        for (int r = 0; r < NY; ++r)
+          if (kc * 32 + ty + 64 / YL * r >= a.BT) ry[r].a = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
         for (int r = 0; r < 4; ++r)
           if (kc * 32 + t0 + 8 * r >= a.BT) {
-            ry[r].a = rx[r] = u32x4{0u, 0u, 0u, 0u};
+            rx[r] = u32x4{0u, 0u, 0u, 0u};
             rs[r] = 0u;
           }
       }
 #pragma unroll
+      for (int r = 0; r < NY; ++r)
+        *reinterpret_cast<u32x4*>(slab + off_dy(ty + 64 / YL * r, 8 * (lane & (YL - 1)))) = ry[r].a;
+#pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int t = t0 + 8 * r;
-        *reinterpret_cast<u32x4*>(slab + off_dy(t, 8 * (lane & 7))) = ry[r].a;
         const float f = act8_mul(rs[r]);
-        char* x = slab + SPLIT_DY + MainBF16::off(t, 16 * (lane & 7));
+        char* x = slab + DY + MainBF16::off(t, 16 * (lane & 7));
         *reinterpret_cast<u32x4*>(x) = act8_bf16x8<XF>(u32x2{rx[r][0], rx[r][1]}, f);
         *reinterpret_cast<u32x4*>(x + 16) = act8_bf16x8<XF>(u32x2{rx[r][2], rx[r][3]}, f);
       }
-      if (kc + SPLIT_WAVES < nk) request(kc + SPLIT_WAVES);
+      if (kc + WAVES < nk) request(kc + WAVES);
       // the wave's own LDS writes before its lanes' reads (the hardware runs a wave's
       // LDS accesses in order)
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        bf16x8 fa[2], fb[4];
+        bf16x8 fa[BI], fb[4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) fa[b] = frag(slab + off_dy(tl, b * 32 + fl) + ks * 16 * SPLIT_ROWS * 2, 4 * SPLIT_ROWS * 2);
+        for (int b = 0; b < BI; ++b) fa[b] = frag(slab + off_dy(tl, b * 32 + fl) + ks * 16 * ROWS * 2, 4 * ROWS * 2);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          fb[b] = frag(slab + SPLIT_DY + MainBF16::off(tl, b * 32 + fl) + ks * 16 * TILE * 2, 4 * TILE * 2);
+          fb[b] = frag(slab + DY + MainBF16::off(tl, b * 32 + fl) + ks * 16 * TILE * 2, 4 * TILE * 2);
 #pragma unroll
-        for (int bi = 0; bi < 2; ++bi)
+        for (int bi = 0; bi < BI; ++bi)
 #pragma unroll
           for (int bj = 0; bj < 4; ++bj)
             acc[bi][bj] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[bi], fb[bj], acc[bi][bj], 0, 0, 0);
@@ -636,17 +649,17 @@ struct Act8Split {
     }
   }
 
-  // The sum of the 8 waves' tiles into the first G tile of LDS: waves 0 - 3 write
-  // theirs, waves 4 - 7 add theirs to those, and the threads add the four.
-  __device__ __forceinline__ static void join(float* sG, const f32x16 (&acc)[2][4]) {
+  // The sum of the waves' tiles into the first G tile of LDS: the first half of the waves
+  // write theirs, the others add theirs to those, and the threads add what results.
+  __device__ __forceinline__ static void join(float* sG, const f32x16 (&acc)[BI][4]) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    float* mine = sG + (wave & 3) * SPLIT_G;
+    float* mine = sG + (wave & (WAVES / 2 - 1)) * G;
     __syncthreads();                             // the slabs are no longer read
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (wave >> 2 == h) {
+      if (wave / (WAVES / 2) == h) {
 #pragma unroll
-        for (int bi = 0; bi < 2; ++bi)
+        for (int bi = 0; bi < BI; ++bi)
 #pragma unroll
           for (int bj = 0; bj < 4; ++bj)
 #pragma unroll
@@ -658,32 +671,37 @@ struct Act8Split {
       __syncthreads();
     }
 #pragma unroll
-    for (int i = threadIdx.x; i < SPLIT_ROWS * TILE / 4; i += 2 * NT) {
+    for (int i = threadIdx.x; i < ROWS * TILE / 4; i += 64 * WAVES) {
       float* p = sG + (i >> 5) * GP + 4 * (i & 31);
       f32x4 g = *reinterpret_cast<f32x4*>(p);
 #pragma unroll
-      for (int k = 1; k < 4; ++k) g += *reinterpret_cast<f32x4*>(p + k * SPLIT_G);
+      for (int k = 1; k < WAVES / 2; ++k) g += *reinterpret_cast<f32x4*>(p + k * G);
       *reinterpret_cast<f32x4*>(p) = g;
     }
     __syncthreads();
   }
 };
 
-template <int OPT, int WF, int MF, int VF>
-__global__ void __launch_bounds__(2 * NT, 1) k_fused_act8_split(const KArgs8 a) {
-  __shared__ __attribute__((aligned(16))) char lds[LDS_SPLIT];
+template <int ROWS, int WAVES, int OPT, int WF, int MF, int VF>
+__global__ void __launch_bounds__(64 * WAVES, 1) k_fused_act8_split(const KArgs8 a) {
+  using M = Act8Split<ROWS, WAVES>;
+  constexpr int ET = 2 * NT;                         // threads of the epilogue
+  constexpr bool EARLY = WAVES == 8;                 // (16 waves have no registers for it)
+  __shared__ __attribute__((aligned(16))) char lds[M::LDS];
   int ti, tj;
   tile_by_xcd((int)gridDim.x / a.tiles_k, a.tiles_k, ti, tj);
-  const int row0 = ti * SPLIT_ROWS, col0 = tj * TILE;
-  f32x16 acc[2][4];
-  if (a.x_fmt == FMT_S8) Act8Split::run<FMT_S8>(a, lds, row0, col0, acc);
-  else Act8Split::run<FMT_E4M3>(a, lds, row0, col0, acc);
-  Epilogue<Step<OPT, WF, MF, VF, false, 0, true>, FMT_NONE, false, 2, 2 * NT, false, false, SPLIT_ROWS> epi;
+  const int row0 = ti * ROWS, col0 = tj * TILE;
+  f32x16 acc[M::BI][4];
+  if (a.x_fmt == FMT_S8) M::template run<FMT_S8>(a, lds, row0, col0, acc);
+  else M::template run<FMT_E4M3>(a, lds, row0, col0, acc);
+  Epilogue<Step<OPT, WF, MF, VF, false, 0, true>, FMT_NONE, false, 2, ET, false, false, ROWS> epi;
   epi.tid = threadIdx.x;
-  epi.prefetch(a, row0, col0);
+  const bool steps = threadIdx.x < ET;               // (whole waves)
+  if (EARLY && steps) epi.prefetch(a, row0, col0);
   float* sG = reinterpret_cast<float*>(lds);
-  Act8Split::join(sG, acc);
-  epi.run_prefetched(a, sG, row0, col0);
+  M::join(sG, acc);
+  if (!EARLY && steps) epi.prefetch(a, row0, col0);
+  if (steps) epi.run_prefetched(a, sG, row0, col0);
 }
 
 template <int OPT, int WF, int MF, int VF>
@@ -708,17 +726,23 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8_tiny(const KArgs8 a) {
 //  - the 256 x 256 tiles (k_fused_act8_wide) pay for long token axes once they fill the
 //    chip: at BT 8192 239 against 302 us for 256 of them (4096 x 4096), but 212
 //    against 109 for 64 (2048 x 2048);
+//  - of the split kernel's two shapes 32 rows and 16 waves win while every tile has a CU
+//    to itself (1024 x 1024: 13.7 against 17.2 us at BT 1024, 46 against 57 at 8192; 336 x
+//    128 33 against 45 at BT 6427), 64 rows and 8 waves beyond (1001 x 1503, 384 tiles of
+//    32 rows: 20.2 against 16.1 us at BT 512, 100 against 72 at 8192);
 //  - everything else of at least 8 x 16 is the split kernel's (3000 x 3000, whose rows
 //    the ring does not take: 290 us at BT 8192, 527 through registers).
 inline bool act8_ring(const KArgs8& a) { return a.x_dma && a.vec_state && a.K % 4 == 0; }
 inline bool act8_split(const KArgs8& a, bool ring) {
   return a.N >= 8 && a.K >= 16 && (!ring || ((int64_t)a.tiles_n * a.tiles_k < 256 && a.BT >= 128));
 }
+inline bool act8_few(const KArgs8& a) { return ((int64_t)a.N + 31) / 32 * a.tiles_k <= 256; }
 inline bool act8_wide(const KArgs8& a) {
   return a.BT >= WIDE_MIN_BT && (int64_t)((a.N + 255) / 256) * ((a.K + 255) / 256) >= 192;
 }
+template <int ROWS>
 inline dim3 split_grid(const KArgs8& a) {
-  return dim3((unsigned)((a.N + SPLIT_ROWS - 1) / SPLIT_ROWS * a.tiles_k));
+  return dim3((unsigned)((a.N + ROWS - 1) / ROWS * a.tiles_k));
 }
 
 template <int XF, int O, int M, int V>
@@ -756,8 +780,13 @@ hipError_t combo_fused_act8(const KArgs8& a, int w_fmt, hipStream_t st) {
   if (w_fmt != FMT_BF16 && w_fmt != FMT_F32) return hipErrorInvalidValue;
   const bool wbf = w_fmt == FMT_BF16, ring = act8_ring(a);
   if (act8_split(a, ring)) {
-    if (wbf) hipLaunchKernelGGL((k_fused_act8_split<O, FMT_BF16, M, V>), split_grid(a), dim3(2 * NT), 0, st, a);
-    else hipLaunchKernelGGL((k_fused_act8_split<O, FMT_F32, M, V>), split_grid(a), dim3(2 * NT), 0, st, a);
+    if (act8_few(a)) {
+      if (wbf) hipLaunchKernelGGL((k_fused_act8_split<32, 16, O, FMT_BF16, M, V>), split_grid<32>(a), dim3(1024), 0, st, a);
+      else hipLaunchKernelGGL((k_fused_act8_split<32, 16, O, FMT_F32, M, V>), split_grid<32>(a), dim3(1024), 0, st, a);
+    } else {
+      if (wbf) hipLaunchKernelGGL((k_fused_act8_split<64, 8, O, FMT_BF16, M, V>), split_grid<64>(a), dim3(512), 0, st, a);
+      else hipLaunchKernelGGL((k_fused_act8_split<64, 8, O, FMT_F32, M, V>), split_grid<64>(a), dim3(512), 0, st, a);
+    }
   } else if (ring) {
     return a.x_fmt == FMT_S8 ? fused_act8_dma<FMT_S8, O, M, V>(a, w_fmt, st)
                              : fused_act8_dma<FMT_E4M3, O, M, V>(a, w_fmt, st);

@@ -181,6 +181,21 @@ def test_step_long_token_axis(fmt, opt, state, w, BT, N, K):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("opt,state,w", [("adamw", "f32", "bf16"), ("adamw", "bf16", "f32"), ("adamw", "int8", "bf16"),
+                                         ("adamw", "e4m3", "f32"), ("lion", "f32", "bf16"), ("sgdm", "bf16", "f32")])
+@pytest.mark.parametrize("BT,N,K", [(300, 2600, 512), (129, 2605, 515), (31, 1001, 1503)])
+def test_step_more_tiles_than_cus(fmt, opt, state, w, BT, N, K):
+    """Over 256 tiles of 32 x 128, under 256 of 128 x 128 or unaligned; sampled rows."""
+    _say(f"case: step act8 tiles {fmt} {opt} {state} {w} {N}x{K} BT {BT}")
+    if K % 128 and state in ("int8", "e4m3"):
+        K = K // 128 * 128
+    L, q, _keep = _layer8(79, N, K, BT, _spec(opt, state, w), fmt, 32)
+    snap, h = snapshot(L, np.array([0, 31, 63, 64, 500, N - 64, N - 1])), _hyper(opt)
+    F.forge_wgrad_step_act8(q, L.dY, L.W, L.forge_m(), L.forge_v(), h, 10, 1337)
+    assert_ok(check_against_oracle(snap, L, h, 10, 1337))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("opt,state,w", [("adamw", "f32", "bf16"), ("adamw", "bf16", "bf16"), ("adamw", "int8", "bf16"),
                                          ("adamw", "e4m3", "f32"), ("lion", "f32", "f32"), ("lion", "bf16", "bf16"),
                                          ("sgdm", "f32", "bf16"), ("sgdm", "bf16", "f32")])
@@ -243,7 +258,7 @@ def test_a_poisoned_block_reaches_the_gradient(BT):
 
 
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("N,K,BT", [(256, 384, 96), (77, 130, 65), (256, 256, 2050), (16, 8, 0), (2048, 2048, 130), (5, 5, 40),
+@pytest.mark.parametrize("N,K,BT", [(256, 384, 96), (77, 130, 65), (256, 256, 2050), (16, 8, 0), (2048, 2048, 130), (5, 5, 40), (2605, 515, 150),
                                     (100, 64, 200)])
 def test_accumulate(fmt, N, K, BT):
     """acc = G within the bound of an fp32 sum in any order; then one fp32 addition of G."""
