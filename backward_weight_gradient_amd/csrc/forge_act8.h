@@ -102,7 +102,13 @@ template <int FMT> struct Raw8;
 template <> struct Raw8<FMT_F32> { f32x4 a, b; };
 template <> struct Raw8<FMT_BF16> { u32x4 a; };
 
-template <int FMT, int MODE = ROW_ANY>
+// STREAM: past the caches, for data that nothing reads again soon.
+template <bool STREAM, class T>
+__device__ __forceinline__ T load_as(const void* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(static_cast<const T*>(p));
+  else return *static_cast<const T*>(p);
+}
+template <int FMT, int MODE = ROW_ANY, bool STREAM = false>
 __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t K) {
   Raw8<FMT> r;
   if constexpr (FMT == FMT_F32) r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -111,20 +117,20 @@ __device__ __forceinline__ Raw8<FMT> row_raw8(const void* p, int64_t c, int64_t 
     if (c < K) {
       if constexpr (FMT == FMT_F32) {
         const float* q = static_cast<const float*>(p) + c;
-        r.a = *reinterpret_cast<const f32x4_u*>(q);
-        r.b = *reinterpret_cast<const f32x4_u*>(q + 4);
+        r.a = load_as<STREAM, f32x4_u>(q);
+        r.b = load_as<STREAM, f32x4_u>(q + 4);
       } else {
-        r.a = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(p) + c);
+        r.a = load_as<STREAM, u32x4_u>(static_cast<const uint16_t*>(p) + c);
       }
     }
   } else if (MODE == ROW_BIG || K >= 8) {
     const int64_t at = min(c, K - 8);
     if constexpr (FMT == FMT_F32) {
       const float* q = static_cast<const float*>(p) + at;
-      r.a = *reinterpret_cast<const f32x4_u*>(q);
-      r.b = *reinterpret_cast<const f32x4_u*>(q + 4);
+      r.a = load_as<STREAM, f32x4_u>(q);
+      r.b = load_as<STREAM, f32x4_u>(q + 4);
     } else {
-      r.a = *reinterpret_cast<const u32x4_u*>(static_cast<const uint16_t*>(p) + at);
+      r.a = load_as<STREAM, u32x4_u>(static_cast<const uint16_t*>(p) + at);
     }
   } else {
     for (int64_t i = K - 1; i >= 0; --i) {   // last element first, each pushing the others up

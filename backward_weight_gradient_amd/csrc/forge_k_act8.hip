@@ -1,7 +1,9 @@
 // Activations to and from 8 bits.  Both directions stream: s bytes read and
 // 1 + 1/block written per element (or the reverse), no arithmetic to speak of,
-// so they are bound by HBM: 8192 x 14336 bf16 and S8 take 65 us to 8 bits and 60 back
-// (354 MB, 5.4 and 5.9 TB/s).
+// so they are bound by HBM: 8192 x 14336 bf16 and S8 take 62 us to 8 bits and 60 back
+// (354 MB, 5.8 TB/s).  X is read past the caches, which leaves them to the codes: both
+// ways in turn take 121 us so, 136 with X through them (8192 x 4096, where all of it
+// fits, 37.5 and 36.2; codes past the caches too: 123 and 40).
 //
 // Thread mapping: a lane owns 8 consecutive columns, so a block of 32, 64 or 128
 // columns is 4, 8 or 16 adjacent lanes of one DPP row, which reduce its absmax
@@ -38,7 +40,7 @@ __device__ __forceinline__ void quantize_unit(const ActArgs& a, int64_t unit) {
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
     const int64_t r = min(r0 + (int64_t)u * rpb, a.rows - 1);   // a row past the end: read again, not stored
-    w[u] = row_raw8<XF, MODE>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K);
+    w[u] = row_raw8<XF, MODE, true>(static_cast<const char*>(a.X) + r * a.ldx * es, c, a.K);
   }
 #pragma unroll
   for (int u = 0; u < ACT_UNR; ++u) {
