@@ -284,6 +284,13 @@ def current_stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+def _device_stream(device: Optional[int]) -> int:
+    """The current stream of a device (None: of the current device)."""
+    if device is None or _raw_stream is None:
+        return current_stream()
+    return _raw_stream(device)
+
+
 def _ref(x):
     return ctypes.byref(x) if x is not None else None
 
@@ -504,17 +511,18 @@ def _launch(name, stream, check, fn, tensors, *args):
         if isinstance(t, forge_act8):
             t = t.tensors and t.tensors[0]
         if isinstance(t, torch.Tensor):
-            if device is None:
-                device = t.device
-                if device.type != "cuda":
-                    raise ValueError(f"{name}: tensors on {device}, expected a GPU")
-            elif t.device != device:
-                raise ValueError(f"{name}: tensors on {device} and {t.device} in one call")
-    if device is None or device.index == torch.cuda.current_device():
-        rc = fn(*args, current_stream() if stream is None else stream)
+            index = t.get_device()
+            if index != device:
+                if index < 0:
+                    raise ValueError(f"{name}: tensors on {t.device}, expected a GPU")
+                if device is not None:
+                    raise ValueError(f"{name}: tensors on cuda:{device} and cuda:{index} in one call")
+                device = index
+    if device is None or device == torch.cuda.current_device():
+        rc = fn(*args, _device_stream(device) if stream is None else stream)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, current_stream() if stream is None else stream)
+            rc = fn(*args, _device_stream(device) if stream is None else stream)
     if rc != FORGE_OK and check:
         raise ForgeError(rc, name)
     return rc
