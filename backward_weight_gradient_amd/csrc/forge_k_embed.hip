@@ -295,26 +295,26 @@ hipError_t launch_embed_sort(const EmbedArgs& e, int64_t tiles, hipStream_t st) 
 // time, 8 lanes of 8 columns each.  The other workgroups take the short rows: a
 // wave per (place that begins a row, ROW_COLS columns), the tokens in order.
 // Every sum has a fixed order.  Bound by HBM for many rows (8192 tokens of 128256 x
-// 4096 added to fp32: 76 us with the sort, 335 MB, 4.4 TB/s), by the latency of the
-// sort and of a row's loads for few (5000 of 1000 x 1001: 12 us, 19 with the sort;
-// half of 8192 tokens on one of 1000 rows of 1024: 40).  Rows are read 8 at a time:
+// 4096 added to fp32: 71 us with the sort, 335 MB, 4.7 TB/s), by the latency of the
+// sort and of a row's loads for few (5000 of 1000 x 1001 bf16: 18 us with the sort;
+// half of 8192 tokens on one of 1000 rows of 1024: 41).  Rows are read 8 at a time:
 // one at a time the last takes 74 us.
 // ------------------------------------------------------------------------
 constexpr int ROW_LONG = 32, ROW_COLS = 512, ROW_SEG = 64;
 
 // End of the run of row v that place p belongs to (keys past the end differ); all
-// lanes of the wave.  64 places in steps of `step`, then 64 in steps of one: two
-// reads find the end of a run of up to 64 step.
-__device__ __forceinline__ int64_t run_end(const EmbedArgs& e, int64_t p, int v, int step) {
+// lanes of the wave.  64 places in steps of 64, then 64 in steps of one: two reads find
+// the end of a run of up to 4096.
+__device__ __forceinline__ int64_t run_end(const EmbedArgs& e, int64_t p, int v) {
   const int lane = threadIdx.x & 63;
   const auto first_other = [&](int64_t at, int64_t by) {   // the first lane whose place is not in the run (64: none)
     const int64_t i = at + lane * by;
     const uint64_t m = __ballot(i >= e.T || e.key[i] != v);
     return m ? __builtin_ctzll(m) : 64;
   };
-  while (step > 1) {
-    const int k = first_other(p, step);
-    p += (int64_t)(k - 1) * step;       // the last place seen inside the run (k > 0: p itself is)
+  for (;;) {
+    const int k = first_other(p, 64);
+    p += (int64_t)(k - 1) * 64;         // the last place seen inside the run (k > 0: p itself is)
     if (k < 64) break;
   }
   for (;;) {
@@ -337,7 +337,7 @@ __device__ __forceinline__ void rows_long(const EmbedArgs& e, float* acc, int64_
   const int64_t q = p - (lane & (ROW_LONG - 1));                    // p, p - 1, .. p - 31
   const uint64_t before = __ballot(q < 0 || e.key[q < 0 ? 0 : q] != v) & 0xFFFFFFFFull;
   const int64_t first = p - (before ? __builtin_ctzll(before) : ROW_LONG) + 1;
-  const int64_t end = run_end(e, p, v, 64);
+  const int64_t end = run_end(e, p, v);
   if (end - first <= ROW_LONG) return;
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   const int slot = wave * 8 + (lane >> 3);
@@ -349,7 +349,8 @@ __device__ __forceinline__ void rows_long(const EmbedArgs& e, float* acc, int64_
     const auto at = [&](int i) {
       return static_cast<const char*>(e.dY) + (int64_t)tok[min(slot + 32 * i, n - 1)] * e.lddy * ds;
     };
-    sum_rows<MODE, DF>(at, (n + 31) / 32, (n - slot + 31) / 32, c, e.K, s);
+    // (half as many fp32 rows at a time: the kernel keeps to 128 registers)
+    sum_rows<MODE, DF, DF == FMT_F32 ? 4 : 8>(at, (n + 31) / 32, (n - slot + 31) / 32, c, e.K, s);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
@@ -374,11 +375,14 @@ template <int MODE, int DF>
 __device__ __forceinline__ void rows_short(const EmbedArgs& e, float* acc, int64_t ldacc, int add, int64_t p, int64_t c0) {
   constexpr int ds = DF == FMT_F32 ? 4 : 2;
   const int lane = threadIdx.x & 63;
-  const int v = e.key[p];
-  if (v >= e.V || (p > 0 && e.key[p - 1] == v)) return;
-  const int n = (int)min((int64_t)(ROW_LONG + 1), run_end(e, p, v, 1) - p);
+  // the 64 places from p on and the one before, requested together
+  const int64_t i = min(p + lane, e.T - 1);
+  const int key = e.key[i], tok = e.perm[i], before = e.key[p > 0 ? p - 1 : 0];
+  const int v = __builtin_amdgcn_readfirstlane(key);
+  if (v >= e.V || (p > 0 && before == v)) return;
+  const uint64_t others = __ballot(p + lane >= e.T || key != v);
+  const int n = others ? __builtin_ctzll(others) : 64;
   if (n > ROW_LONG) return;
-  const int tok = lane < n ? e.perm[p + lane] : 0;
   static_assert(ROW_COLS == 64 * 8, "a wave's columns");
   const int64_t c = c0 + 8 * lane;
   float* o = acc + (int64_t)v * ldacc;
@@ -401,7 +405,7 @@ __device__ __forceinline__ void rows_short(const EmbedArgs& e, float* acc, int64
 }
 
 template <int MODE, int DF>
-__global__ void __launch_bounds__(NT) k_embed_rows(const EmbedArgs e, float* acc, int64_t ldacc, int add, int longs) {
+__global__ void __launch_bounds__(NT, 4) k_embed_rows(const EmbedArgs e, float* acc, int64_t ldacc, int add, int longs) {
   __shared__ float sum[4][ROW_SEG];
   __shared__ int32_t tok[ROW_PERM];
   if ((int)blockIdx.x < longs) {
