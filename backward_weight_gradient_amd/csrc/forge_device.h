@@ -792,7 +792,7 @@ __device__ __forceinline__ void tile_gradient_by(const A& a, char* lds, int row0
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
 
-  const int nk = (a.BT + M::TK - 1) / M::TK;
+  const int nk = token_chunks(a.BT, M::TK);
   M ml;
   if (nk > 0) {
     ml.load(a, 0, row0, col0);

@@ -47,6 +47,14 @@ struct EpiConst {
   uint32_t sr;     // all ones: stochastic rounding of bf16 (and E4M3 weight) stores, 0: round to nearest even
 };
 
+// Chunks of tk tokens that bt tokens take, for every bt that an int32 holds (bt + tk - 1
+// itself may pass 2^31 - 1).
+constexpr int32_t token_chunks(int32_t bt, int32_t tk) {
+  return (int32_t)(((uint32_t)bt + (uint32_t)tk - 1u) / (uint32_t)tk);
+}
+static_assert(token_chunks(0, 64) == 0 && token_chunks(1, 64) == 1 && token_chunks(64, 64) == 1 &&
+              token_chunks(INT32_MAX, 64) == 1 << 25 && token_chunks(INT32_MAX, 32) == 1 << 26, "every token count");
+
 // Everything a launch needs.  Pointers are device pointers; leading
 // dimensions are in elements.
 struct KArgs {

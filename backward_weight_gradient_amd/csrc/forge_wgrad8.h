@@ -572,7 +572,7 @@ struct Act8Split {
       for (int bj = 0; bj < 4; ++bj)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[bi][bj][e] = 0.f;
-    const int nk = (a.BT + 31) / 32;
+    const int nk = token_chunks(a.BT, 32);
     const int t0 = lane >> 3, ty = lane / YL;      // X: tokens t0 + 8 r of a chunk; dY: ty + 64 / YL r
     const int64_t cy = row0 + 8 * (lane & (YL - 1)), cx = col0 + 16 * (lane & 7);
     const int64_t sx = min(cx, (int64_t)a.K - 1) >> a.x8.sh;
@@ -605,7 +605,7 @@ struct Act8Split {
 #pragma unroll
         for (int r = 0; r < 4; ++r) rx[r] = codes_shift16(rx[r], ex);
       }
-      if (kc * 32 + 32 > a.BT) {   // tokens past the end
+      if (a.BT - kc * 32 < 32) {   // tokens past the end
 #pragma unroll
         for (int r = 0; r < NY; ++r)
           if (kc * 32 + ty + 64 / YL * r >= a.BT) ry[r].a = u32x4{0u, 0u, 0u, 0u};

@@ -1,0 +1,31 @@
+"""GPU: the step from 8-bit X at the ends of its documented sizes."""
+
+import pytest
+import torch
+
+import backward_weight_gradient_amd as F
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("BT", [2 ** 31 - 1])
+def test_token_counts_up_to_2_31(BT):
+    """The longest token axis: all tokens but a few are zeros, the last one among the others.
+    Every product and sum is a small integer, so G is exact."""
+    print(f"case: accumulate act8 8x16 BT {BT}", flush=True)
+    N, K = 8, 16
+    dY = torch.zeros((BT, N), dtype=torch.bfloat16, device="cuda")
+    codes = torch.zeros((BT, K), dtype=torch.int8, device="cuda")
+    scale = torch.full((BT, 1), 127, dtype=torch.uint8, device="cuda")      # 2^0
+    at = torch.tensor([0, 1, 2 ** 30 + 5, BT - 70, BT - 33, BT - 32, BT - 31, BT - 2, BT - 1], device="cuda")
+    g = torch.Generator()
+    g.manual_seed(1)
+    d = torch.randint(-8, 9, (len(at), N), generator=g).cuda()
+    x = torch.randint(-100, 101, (len(at), K), generator=g).cuda()
+    dY[at] = d.to(torch.bfloat16)
+    codes[at] = x.to(torch.int8)
+    acc = torch.full((N, K), float("nan"), device="cuda")
+    F.forge_wgrad_accumulate_act8(F.act8(codes, scale, 32), dY, acc, True)
+    assert torch.equal(acc.double().cpu(), d.double().cpu().t() @ x.double().cpu())
+    del dY, codes, scale
+    torch.cuda.empty_cache()
