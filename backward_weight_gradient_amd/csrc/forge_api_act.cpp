@@ -186,7 +186,9 @@ forge_status forge_rmsnorm(const forge_mat* X, const forge_mat* R, const forge_m
   if (Q && (st = check_act8(*Q, rows, cols)) != FORGE_OK) return st;
   if (R && R->dtype != H->dtype) return FORGE_E_DTYPE;
   if (rows >= kMax31 || cols >= kMax31) return FORGE_E_SHAPE;
-  if (!std::isfinite(eps) || eps < 0) return FORGE_E_HYPER;
+  // the kernels add eps in fp32: a positive one must stay positive and finite there
+  const float eps32 = (float)eps;
+  if (!std::isfinite(eps32) || eps < 0 || (eps32 == 0.f && eps != 0)) return FORGE_E_HYPER;
   if (!aligned(rstd, 4)) return FORGE_E_ALIGN;
   Uses u;
   if (!same_mat(H, X)) u.add(mat_range(*X), false);
@@ -212,7 +214,7 @@ forge_status forge_rmsnorm(const forge_mat* X, const forge_mat* R, const forge_m
   if (Q) { a.q = act8_args(*Q); a.q_fmt = Q->q.dtype; }
   a.rstd = rstd;
   a.rows = rows; a.K = (int32_t)cols;
-  a.eps = (float)eps;
+  a.eps = eps32;
   return hip_status(launch_rmsnorm(a, (hipStream_t)stream));
 }
 

@@ -452,10 +452,13 @@ forge_status forge_wgrad_accumulate_act8(const forge_act8* X, const forge_mat* d
  * Y     : [rows, cols] BF16 (nearest even) or F32, or NULL.
  * Q     : as forge_act_quantize writes it, or NULL.
  * rstd  : rows floats (s, which the backward pass reads), or NULL.
- * eps   : finite, >= 0.  rows, cols < 2^31.
+ * eps   : >= 0; it is rounded to fp32, where it must be finite and may be 0 only
+ *         if it is 0.  rows, cols < 2^31.
  * At least one of H, Y, Q, rstd must be given (else E_NULL).  No rows or no
  * columns: a no-op.  The mean is taken in fp32: a row whose sum of squares passes
- * its range (|H| from about 1e19 on) has s = 0.
+ * its range (|H| from about 1e19 on) has s = 0.  With eps = 0 a row of zeros, or
+ * one whose squares are zero in fp32 (|H| below about 1e-23), has s infinite and
+ * Y NaN; any eps of the usual size covers both.
  * Errors: FORGE_E_NULL, E_SHAPE, E_DTYPE, E_ALIGN, E_HYPER (eps), E_ALIAS
  * (nothing enqueued) or E_HIP.
  */
