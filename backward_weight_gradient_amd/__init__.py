@@ -59,7 +59,7 @@ class forge_mat(ctypes.Structure):
 
 class forge_state(ctypes.Structure):
     _fields_ = [("q", forge_mat), ("scale", ctypes.c_void_p), ("block", ctypes.c_int32)]
-    tensors = ()     # act8(): the tensors behind the addresses
+    tensors = ()     # state(): the tensors behind the addresses
 
 
 class forge_act8(ctypes.Structure):
@@ -232,9 +232,12 @@ def state(t, scale=None, block: int = 0) -> forge_state:
     """A forge_state: values (f32 / bf16), or 8-bit codes (int8 / uint8 / E4M3)
     plus fp32 block scales.  The scale tensor must be float32, contiguous, on
     t's device, with rows * cols / block elements, block in {32, 64, 128}:
-    the kernels read and write exactly that many scales through its pointer."""
+    the kernels read and write exactly that many scales through its pointer.
+    It keeps both tensors alive."""
     if scale is None:
-        return forge_state(mat(t), None, 0)
+        s = forge_state(mat(t), None, 0)
+        s.tensors = (t,)     # the struct holds addresses only: keep their memory while it lives
+        return s
     if block not in (32, 64, 128):
         raise ValueError(f"state: block must be 32, 64 or 128, got {block}")
     if t.dim() != 2 or t.shape[1] % block:
@@ -243,7 +246,9 @@ def state(t, scale=None, block: int = 0) -> forge_state:
         raise ValueError("state: the scale tensor must be contiguous float32 on the codes' device")
     if scale.numel() != t.shape[0] * (t.shape[1] // block):
         raise ValueError(f"state: {scale.numel()} scales given, {t.shape[0] * (t.shape[1] // block)} needed")
-    return forge_state(mat(t), scale.data_ptr() or None, block)
+    s = forge_state(mat(t), scale.data_ptr() or None, block)
+    s.tensors = (t, scale)
+    return s
 
 
 def act8(codes, scale, block: int) -> forge_act8:
@@ -508,8 +513,8 @@ def _launch(name, stream, check, fn, tensors, *args):
     about theirs).  Without a stream: that device's current one."""
     device = None
     for t in tensors:
-        if isinstance(t, forge_act8):
-            t = t.tensors and t.tensors[0]
+        if isinstance(t, (forge_act8, forge_state)):
+            t = t.tensors and t.tensors[0]     # (its scales are on the same device)
         if isinstance(t, torch.Tensor):
             index = t.get_device()
             if index != device:
@@ -579,7 +584,7 @@ def forge_act_dequantize(Q: forge_act8, X, stream=None, check: bool = True) -> i
 def forge_wgrad_step_act8(X: forge_act8, dY, W, m, v, h: forge_hyper, step: int, seed: int, stream=None,
                           check: bool = True) -> int:
     """forge_wgrad_step with X from its 8-bit copy (dY bf16)."""
-    return _launch("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, (dY, W, X), _ref(X),
+    return _launch("forge_wgrad_step_act8", stream, check, lib.forge_wgrad_step_act8, (dY, W, X, m, v), _ref(X),
                    _ref(_as_mat(dY)), _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed)
 
 
@@ -653,7 +658,7 @@ def forge_embed_step(ids, dY, W, m, v, h: forge_hyper, step: int, seed: int, sca
     row of W, in place on W / m / v."""
     ptr, width, T = _ids(ids)
     ws, nbytes = _workspace(workspace)
-    return _launch("forge_embed_step", stream, check, lib.forge_embed_step, (ids, dY, W, workspace), ptr, width, T,
+    return _launch("forge_embed_step", stream, check, lib.forge_embed_step, (ids, dY, W, m, v, workspace), ptr, width, T,
                    _ref(_as_mat(dY)), scale, _ref(_as_mat(W)), _ref(m), _ref(v), _ref(h), step, seed, ws, nbytes)
 
 

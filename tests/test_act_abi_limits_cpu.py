@@ -42,3 +42,47 @@ def test_rmsnorm_eps_outside_fp32(eps):
 @pytest.mark.parametrize("eps", [0.0, 2.0 ** -149, 1e-5, 1.0, 3.4e38])
 def test_rmsnorm_eps_inside_fp32(eps):
     assert norm(eps, rows=0) == F.FORGE_OK
+
+
+# ---------------------------------------------------------------- the states' memory
+def _on(index, t):
+    """t as if it were on GPU `index`."""
+    class Placed(torch.Tensor):
+        def get_device(self):
+            return index
+    return t.as_subclass(Placed)
+
+
+def _steps(m, v, h):
+    """The two steps with every operand but the states given by address."""
+    raw = mat(0, 4, 64, F.FORGE_F32)
+    q = F.forge_act8(mat(1, 4, 64, F.FORGE_S8), addr(2), 64)
+    yield lambda: F.forge_wgrad_step_act8(q, mat(3, 4, 4), raw, m, v, h, 1, 0, stream=S0)
+    yield lambda: F.forge_embed_step(_on(0, torch.zeros(4, dtype=torch.int64)), raw, mat(4, 4, 64), m, v, h, 1, 0, stream=S0)
+
+
+@pytest.mark.parametrize("host", ["m", "v", "codes"])
+def test_states_on_the_host_are_refused(host):
+    """A state's host address would be read and written by the kernel."""
+    t, gpu = torch.zeros(4, 64), _on(0, torch.zeros(4, 64))
+    if host == "codes":
+        m = F.state(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 1), 64)
+        v = F.state(torch.zeros(4, 64, dtype=torch.uint8), torch.zeros(4, 1), 64)
+    else:
+        m, v = F.state(t if host == "m" else gpu), F.state(t if host == "v" else gpu)
+    for call in _steps(m, v, F.hyper()):
+        with pytest.raises(ValueError, match="expected a GPU"):
+            call()
+
+
+def test_states_on_another_gpu_are_refused():
+    m, v = (F.state(_on(i, torch.zeros(4, 64))) for i in (0, 1))
+    for call in _steps(m, v, F.hyper()):
+        with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+            call()
+
+
+def test_a_state_keeps_its_tensors():
+    q, s = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 1)
+    assert F.state(q, s, 64).tensors[0] is q and F.state(q, s, 64).tensors[1] is s
+    assert F.state(s).tensors[0] is s
