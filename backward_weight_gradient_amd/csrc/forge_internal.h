@@ -353,7 +353,9 @@ hipError_t launch_rmsnorm_backward(const NormBwdArgs& a, hipStream_t stream);
 // forge_k_embed.hip.  Tokens sorted by id: key[i] (the row), perm[i] (the token), i < T.
 // Padding tokens have key V and so come last.
 constexpr int EMBED_PART = 8192;   // tokens sorted together in LDS
-constexpr int64_t EMBED_MAX_TOKENS = 1ll << 27, EMBED_MAX_TILES = 1ll << 24;   // a launch has fewer than 2^32 threads
+// A launch has fewer than 2^32 threads (asserted where the sort's is formed).  The ranks across
+// the sort's parts grow with the square of the tokens: 2^22 take 16 ms, the limit some 0.3 s.
+constexpr int64_t EMBED_MAX_TOKENS = 1ll << 24, EMBED_MAX_TILES = 1ll << 24;
 constexpr int EMBED_ROWS = 16;     // rows of the step's tiles
 struct EmbedArgs {
   const void* ids; int32_t id_bytes;

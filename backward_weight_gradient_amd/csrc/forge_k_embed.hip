@@ -144,6 +144,9 @@ hipError_t launch_embed(const void* ids, int id_bytes, int64_t T, const void* W,
 // ------------------------------------------------------------------------
 constexpr int PLACE_TOKENS = 32;     // 2 per thread: an LDS read serves two counts
 constexpr int PLACE_NT = 1024, PLACE_WAVES = PLACE_NT / 64, PLACE_STEP = 4 * PLACE_NT / 16;
+constexpr int64_t PLACE_ZERO_WGS = 1 << 20;   // most workgroups that clear
+static_assert((EMBED_MAX_TOKENS / PLACE_TOKENS + EMBED_MAX_TILES / PLACE_TOKENS + 1 + PLACE_ZERO_WGS) * PLACE_NT < (1ll << 32),
+              "fewer than 2^32 threads");
 
 // bounds: tile[i] = the first place whose row is >= i * EMBED_ROWS, for i = 0 .. bounds - 1.
 struct SortArgs {
@@ -273,7 +276,7 @@ static hipError_t sort_tokens(const EmbedArgs& e, int64_t bounds, const ZeroArgs
     a.place_wgs = (int32_t)((a.parts - 1) * (EMBED_PART / PLACE_TOKENS) + (last + PLACE_TOKENS - 1) / PLACE_TOKENS);
     if (a.parts == 1) a.bound_wgs = (int32_t)((bounds + PLACE_TOKENS - 1) / PLACE_TOKENS);
   }
-  const int64_t per = PLACE_NT >> zero.sh, zero_wgs = std::min<int64_t>((zero.rows + per - 1) / per, 1 << 20);
+  const int64_t per = PLACE_NT >> zero.sh, zero_wgs = std::min<int64_t>((zero.rows + per - 1) / per, PLACE_ZERO_WGS);
   const unsigned grid = (unsigned)(a.place_wgs + a.bound_wgs + zero_wgs);
   if (grid == 0) return hipSuccess;
   hipLaunchKernelGGL(k_embed_place, dim3(grid), dim3(PLACE_NT), 0, st, a);

@@ -508,7 +508,7 @@ int64_t forge_rmsnorm_workspace_bytes(int64_t rows, int64_t cols);
  * h, step, seed, combinations and limits as forge_wgrad_step.
  * workspace: forge_embed_workspace_bytes(T, V) bytes, 16-byte aligned scratch.
  * Calls that may overlap need their own.
- * V, K < 2^31, T < 2^31 for forge_embed, T < 2^27 for the gradient; for the step
+ * V, K < 2^31, T < 2^31 for forge_embed, T < 2^24 for the gradient; for the step
  * V * K < 2^32 and ceil(V / 16) * ceil(K / 128) < 2^24.  T may be 0 (G = 0).
  * Errors: FORGE_E_NULL, E_SHAPE (id_bytes, sizes, workspace too small), E_DTYPE,
  * E_ALIGN, E_HYPER (scale not finite), E_ALIAS, and those of forge_wgrad_step

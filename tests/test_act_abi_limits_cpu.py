@@ -86,3 +86,17 @@ def test_a_state_keeps_its_tensors():
     q, s = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 1)
     assert F.state(q, s, 64).tensors[0] is q and F.state(q, s, 64).tensors[1] is s
     assert F.state(s).tensors[0] is s
+
+
+# ---------------------------------------------------------------- embedding
+def embed_accumulate(T, V, K=8):
+    return rc("forge_embed_accumulate", addr(0), 8, T, mat(1, T, K), 1.0, mat(2, V, K, F.FORGE_F32), 1, addr(7), 1 << 36, S0)
+
+
+def test_embedding_gradient_token_limit():
+    """2^24 tokens: the sort's launch, with its clearing workgroups, stays below 2^32 threads
+    (checked where it is compiled) and its cost, quadratic in the end, below a second."""
+    for V in (1, 1000, 2 ** 31 - 2):
+        assert F.forge_embed_workspace_bytes(2 ** 24 - 1, V) > 0 and F.forge_embed_workspace_bytes(2 ** 24, V) == 0
+        assert embed_accumulate(2 ** 24, V, 1) == F.FORGE_E_SHAPE
+        assert embed_accumulate(2 ** 27 - 1, V, 1) == F.FORGE_E_SHAPE

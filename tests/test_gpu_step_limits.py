@@ -29,3 +29,20 @@ def test_token_counts_up_to_2_31(BT):
     assert torch.equal(acc.double().cpu(), d.double().cpu().t() @ x.double().cpu())
     del dY, codes, scale
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [2 ** 24 - 1])
+def test_embedding_gradient_of_the_most_tokens(T):
+    """The sort's largest launch.  Values are small integers: G is exact."""
+    V, K = 100003, 8
+    print(f"case: embedding gradient {T} of {V}x{K}", flush=True)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    ids = torch.randint(-1, V + 1, (T,), generator=g, device="cuda")
+    dY = torch.randint(-8, 9, (T, K), generator=g, device="cuda").to(torch.bfloat16)
+    acc = torch.full((V, K), float("nan"), device="cuda")
+    ws = torch.empty(F.forge_embed_workspace_bytes(T, V), dtype=torch.uint8, device="cuda")
+    F.forge_embed_accumulate(ids, dY, acc, True, workspace=ws)
+    ok = (ids >= 0) & (ids < V)
+    want = torch.zeros((V, K), dtype=torch.float64, device="cuda").index_add_(0, ids[ok], dY[ok].double())
+    assert torch.equal(acc.double(), want)
