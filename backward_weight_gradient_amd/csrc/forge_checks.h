@@ -125,6 +125,9 @@ struct Plan {
   bool empty = false;  // N == 0 or K == 0: nothing to do
 };
 
+// A launch takes fewer than 2^32 threads: 2^24 workgroups of 256, one for each tile.
+bool too_many_tiles(const Plan& pl) { return ((pl.N + 127) / 128) * ((pl.K + 127) / 128) >= (1ll << 24); }
+
 forge_status check_state(const forge_state& s, int64_t N, int64_t K, bool first, Plan& pl) {
   forge_status st = check_mat(s.q, N, K);
   if (st != FORGE_OK) return st;
@@ -220,8 +223,7 @@ forge_status validate(const forge_mat* X, const forge_mat* dY, const forge_mat* 
   // size limits: 32-bit flat SR index and 32-bit tile / token counters
   if ((uint64_t)pl.N * (uint64_t)pl.K >= (1ull << 32)) return FORGE_E_SHAPE;
   if (pl.BT >= (1ll << 31) || pl.N >= (1ll << 31) || pl.K >= (1ll << 31)) return FORGE_E_SHAPE;
-  const int64_t tiles = ((pl.N + 127) / 128) * ((pl.K + 127) / 128);
-  if (tiles >= (1ll << 31)) return FORGE_E_SHAPE;
+  if (too_many_tiles(pl)) return FORGE_E_SHAPE;
   // aliasing: outputs must not overlap inputs or each other
   Range outs[5], ins[2];
   layer_ranges(X, dY, W, m, v, pl, outs, ins);
@@ -273,6 +275,7 @@ forge_status validate_inputs(const forge_mat* X, const forge_mat* dY, Plan& pl, 
   }
   if ((uint64_t)pl.N * (uint64_t)pl.K >= (1ull << 32)) return FORGE_E_SHAPE;
   if (pl.BT >= (1ll << 31) || pl.N >= (1ll << 31) || pl.K >= (1ll << 31)) return FORGE_E_SHAPE;
+  if (too_many_tiles(pl)) return FORGE_E_SHAPE;
   pl.in_fmt = dY->dtype;
   pl.empty = (pl.N == 0 || pl.K == 0);
   return FORGE_OK;

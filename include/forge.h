@@ -158,7 +158,8 @@ typedef struct {
  *   RMSprop / AdaGrad v in {F32, BF16}, or SGD (no state).
  *   A missing required state is E_NULL, a state the optimizer does not keep
  *   is E_UNSUPPORTED.
- * Int8 and E4M3 states need K % block == 0.  N * K must be < 2^32 (flat SR index).
+ * Int8 and E4M3 states need K % block == 0.  N * K must be < 2^32 (flat SR index),
+ * BT, N, K < 2^31 and ceil(N / 128) * ceil(K / 128) < 2^24 (one launch).
  * BT may be 0 (G = 0: the step still applies decay / momentum).
  * N == 0 or K == 0 is a no-op.
  *

@@ -100,3 +100,24 @@ def test_embedding_gradient_token_limit():
         assert F.forge_embed_workspace_bytes(2 ** 24 - 1, V) > 0 and F.forge_embed_workspace_bytes(2 ** 24, V) == 0
         assert embed_accumulate(2 ** 24, V, 1) == F.FORGE_E_SHAPE
         assert embed_accumulate(2 ** 27 - 1, V, 1) == F.FORGE_E_SHAPE
+
+
+# ---------------------------------------------------------------- launch sizes
+@pytest.mark.parametrize("N,K", [(1, 2 ** 31 - 1), (2 ** 31 - 1, 2), (2, 2 ** 31 - 127)])
+def test_layers_of_2_24_tiles_are_refused(N, K):
+    """2^24 workgroups of 256 threads are 2^32, more than a launch takes."""
+    X, X8 = mat(0, 4, K), F.forge_act8(mat(0, 4, K, F.FORGE_S8), addr(9), 32)
+    dY, W, m, v = mat(1, 4, N), mat(2, N, K), *(F.forge_state(mat(i, N, K, F.FORGE_F32), None, 0) for i in (3, 4))
+    assert F.forge_wgrad_check(X, dY, W, m, v, F.hyper(), 1) == F.FORGE_E_SHAPE
+    assert F.forge_wgrad_check_act8(X8, dY, W, m, v, F.hyper(), 1) == F.FORGE_E_SHAPE
+    acc = mat(5, N, K, F.FORGE_F32)
+    assert rc("forge_wgrad_accumulate", X, dY, acc, 1, S0) == F.FORGE_E_SHAPE
+    assert rc("forge_wgrad_accumulate_act8", X8, dY, acc, 1, S0) == F.FORGE_E_SHAPE
+
+
+@pytest.mark.parametrize("N,K", [(1, 2 ** 31 - 128), (2 ** 31 - 128, 2), (2 ** 16 - 1, 2 ** 16)])
+def test_layers_of_fewer_tiles_are_accepted(N, K):
+    X, X8 = mat(0, 4, K), F.forge_act8(mat(0, 4, K, F.FORGE_S8), addr(9), 32)
+    dY, W, m, v = mat(1, 4, N), mat(2, N, K), *(F.forge_state(mat(i, N, K, F.FORGE_F32), None, 0) for i in (3, 4))
+    assert F.forge_wgrad_check(X, dY, W, m, v, F.hyper(), 1) == F.FORGE_OK
+    assert F.forge_wgrad_check_act8(X8, dY, W, m, v, F.hyper(), 1) == F.FORGE_OK
