@@ -93,7 +93,7 @@ forge_status check_embed_grad(const void* ids, int32_t id_bytes, int64_t T, cons
   if (!dY) return FORGE_E_NULL;
   forge_status st = check_ids(ids, id_bytes, T);
   if (st != FORGE_OK) return st;
-  if (V < 0 || K < 0 || V >= kMax31 - 1 || K >= kMax31 || T >= EMBED_MAX_TOKENS) return FORGE_E_SHAPE;
+  if (V < 0 || K < 0 || V >= kMax31 || K >= kMax31 || T >= EMBED_MAX_TOKENS) return FORGE_E_SHAPE;
   if ((st = check_float_mat(dY, T, K)) != FORGE_OK) return st;
   if (!std::isfinite((float)scale)) return FORGE_E_HYPER;
   const int64_t need = V > 0 && K > 0 ? forge_embed_workspace_bytes(T, V) : 0;
@@ -287,7 +287,7 @@ forge_status forge_embed(const void* ids, int32_t id_bytes, int64_t T, const for
 }
 
 int64_t forge_embed_workspace_bytes(int64_t T, int64_t V) {
-  if (T < 0 || V <= 0 || T >= EMBED_MAX_TOKENS || V >= kMax31 - 1) return 0;
+  if (T < 0 || V <= 0 || T >= EMBED_MAX_TOKENS || V >= kMax31) return 0;
   return 2 * round16(4 * T) + round16(4 * (V / EMBED_ROWS + 2)) + (T > EMBED_PART ? 8 * T : 0);
 }
 

@@ -121,3 +121,12 @@ def test_layers_of_fewer_tiles_are_accepted(N, K):
     dY, W, m, v = mat(1, 4, N), mat(2, N, K), *(F.forge_state(mat(i, N, K, F.FORGE_F32), None, 0) for i in (3, 4))
     assert F.forge_wgrad_check(X, dY, W, m, v, F.hyper(), 1) == F.FORGE_OK
     assert F.forge_wgrad_check_act8(X8, dY, W, m, v, F.hyper(), 1) == F.FORGE_OK
+
+
+def test_embedding_gradient_takes_every_vocabulary_below_2_31():
+    V = 2 ** 31 - 1
+    assert F.forge_embed_workspace_bytes(10, V) > 0 and F.forge_embed_workspace_bytes(10, V + 1) == 0
+    assert embed_accumulate(10, V + 1, 1) == F.FORGE_E_SHAPE
+    ws = F.forge_embed_workspace_bytes(10, V)
+    small = rc("forge_embed_accumulate", addr(0), 8, 10, mat(1, 10, 1), 1.0, mat(2, V, 1, F.FORGE_F32), 1, addr(7) + 8, ws, S0)
+    assert small == F.FORGE_E_ALIGN        # the sizes passed

@@ -46,3 +46,21 @@ def test_embedding_gradient_of_the_most_tokens(T):
     ok = (ids >= 0) & (ids < V)
     want = torch.zeros((V, K), dtype=torch.float64, device="cuda").index_add_(0, ids[ok], dY[ok].double())
     assert torch.equal(acc.double(), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_embedding_gradient_of_the_largest_vocabulary(dtype):
+    """2^31 - 1 rows of one column; the id 2^31 - 1 is padding."""
+    V = 2 ** 31 - 1
+    print(f"case: embedding gradient of {V} rows, {dtype}", flush=True)
+    ids = torch.tensor([V - 1, V, -1, 0, V - 1, 2 ** 30, V, V - 2, 0, 7], device="cuda").to(dtype)
+    dY = torch.tensor([1.0, 100, 200, 3, 4, 5, 300, 6, 7, 8], device="cuda")[:, None].contiguous()
+    acc = torch.full((V, 1), float("nan"), device="cuda")
+    ws = torch.empty(F.forge_embed_workspace_bytes(10, V), dtype=torch.uint8, device="cuda")
+    F.forge_embed_accumulate(ids, dY, acc, True, workspace=ws)
+    for row, g in ((V - 1, 5.0), (V - 2, 6.0), (2 ** 30, 5.0), (0, 10.0), (7, 8.0)):
+        assert acc[row].item() == g
+        acc[row] = 0
+    assert not bool(acc.any())
+    del acc
+    torch.cuda.empty_cache()
