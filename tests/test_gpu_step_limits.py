@@ -64,3 +64,41 @@ def test_embedding_gradient_of_the_largest_vocabulary(dtype):
     assert not bool(acc.any())
     del acc
     torch.cuda.empty_cache()
+
+
+def test_longest_rows():
+    """One row (two for the lookup) of 2^31 - 1 columns through the copies, the norm, and the embedding."""
+    K = 2 ** 31 - 1
+    print(f"case: rows of {K} columns", flush=True)
+    x = torch.empty((1, K), dtype=torch.bfloat16, device="cuda")
+    x[0] = (torch.arange(K, device="cuda", dtype=torch.int32) % 127 - 63).to(torch.bfloat16)
+    x[0, K - 2] = 126
+    codes, scale = torch.empty((1, K), dtype=torch.int8, device="cuda"), torch.empty((1, 2 ** 24), dtype=torch.uint8, device="cuda")
+    back = torch.empty_like(x)
+    q = F.act8(codes, scale, 128)
+    F.forge_act_quantize(x, q)
+    F.forge_act_dequantize(q, back)
+    # |x| <= 63: 2^-1 resolves halves; the last block, of 127 columns up to 126, has 2^0
+    assert torch.equal(back, x) and scale[0, -1].item() == 127 and bool((scale[0, :-1] == 126).all())
+    # the same row as a gradient and as a weight
+    acc = torch.full((1, K), float("nan"), device="cuda")
+    ids = torch.tensor([0, 0], device="cuda")
+    F.forge_embed_accumulate(ids, x.expand(2, K).contiguous(), acc, True, workspace=torch.empty(
+        F.forge_embed_workspace_bytes(2, 1), dtype=torch.uint8, device="cuda"))
+    assert torch.equal(acc.bfloat16(), x + x) and acc[0, K - 1].item() == 2 * x[0, K - 1].item()
+    del acc
+    y = torch.full((2, K), 9.0, dtype=torch.bfloat16, device="cuda")
+    F.forge_embed(torch.tensor([1, 0], device="cuda"), x, y, scale=2.0)
+    assert not bool(y[0].any()) and torch.equal(y[1], (x + x)[0])
+    del y
+    # the norm of a row of ones but for its last columns: powers of two, exact products; the sum of squares,
+    # 2^21 terms a thread and 16 lanes and waves after them, is within (2^21 + 40) 2^-24 of K
+    x.fill_(1.0)
+    rstd, one, h = torch.empty(1, device="cuda"), torch.ones(K, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x)
+    F.forge_rmsnorm(x, one, back, rstd=rstd)
+    assert abs(rstd.item() - 1) <= 0.5 * (2 ** 21 + 40) * 2.0 ** -24 + 1e-5
+    assert torch.equal(back, (x * rstd).bfloat16())
+    F.forge_rmsnorm_backward(x, x, one, torch.ones(1, device="cuda"), h)
+    # dX = g - n mean(g n) = 1 - mean: the mean's sum as above
+    assert float(h.abs().max()) <= (2 ** 21 + 40) * 2.0 ** -24 and bool((h == h[0, 0]).all())
+    torch.cuda.empty_cache()
