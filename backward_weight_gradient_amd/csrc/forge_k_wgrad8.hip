@@ -64,7 +64,10 @@ __global__ void __launch_bounds__(NT, 2) k_gemm_act8_tiny(const KArgs8 a) {
   store_g<TILE, NT>(a, reinterpret_cast<const float*>(lds), ti * TILE, tj * TILE);
 }
 
-// The same choice as for the step (the accumulator's rows may be of any alignment).
+// As for the step, but without the 256 x 256 tiles, which no accumulation has: 4096 x 4096,
+// BT 8192 takes 314 us on the ring from S8 X and 265 from bf16 X, gate_proj at BT 512 105 and
+// 91 (the step itself 266 and 248, 222 and 216).  The accumulator's rows may be of any
+// alignment.
 hipError_t launch_gemm_act8(const KArgs8& a, hipStream_t st) {
   if (act8_split(a, a.x_dma) && act8_few(a))
     hipLaunchKernelGGL((k_gemm_act8_split<32, 16>), split_grid<32>(a), dim3(1024), 0, st, a);
