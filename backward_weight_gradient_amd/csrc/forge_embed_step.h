@@ -110,14 +110,17 @@ __global__ void __launch_bounds__(NT, 4) k_embed_step(const KArgs a, const Embed
 // FAST: rows of whole 128-byte lines, whose accesses bypass the caches and whose
 // tiles go out row of tiles by row.  Other rows share lines at the tiles' seams, and
 // streaming parts of lines through different XCDs costs far more than the lines
-// themselves: with tiles of 128 rows 37929 x 2984 took 629 us so, 337 with cached
-// accesses and neighbouring tiles on one XCD (46421 x 1459 530 and 316).
+// themselves: with tiles of 128 rows 37929 x 2984 (bf16 moments, 161 tokens) took 629 us so,
+// 337 with cached accesses and neighbouring tiles on one XCD (46421 x 1459, fp32 moments, 124
+// tokens: 530 and 316).
 //
 // Tiles of 16 rows, four workgroups to a CU: small ones hide each other's gathering.
 // With AdamW, bf16 W and fp32 moments 8192 tokens of 128256 x 4096 take 1773 us (10.6 GB,
 // 6.0 TB/s: bound by HBM), 1837 with tiles of 128 rows; 8192 of 32000 x 4096 458 and 502
 // (two workgroups to a CU: 500); 4096 of 1000 x 1024, bound by latency, 17 and 44; the
-// unaligned 46421 x 1459 280 and 313, 37929 x 2985 316 and 352.
+// unaligned 46421 x 1459 with 124 tokens 280 and 313, 37929 x 2985 with bf16 moments and 161
+// tokens 316 and 352.  Tokens cost more where the state is small: the last takes 284 us with
+// 100 tokens, 338 with 1000, 470 with 8192 (spread over the vocabulary).
 template <int O, int M, int V>
 hipError_t combo_embed(const KArgs& a, const EmbedArgs& e, int w_fmt, hipStream_t st) {
   const bool fast = a.vec_state && a.K % 64 == 0 && a.ldw % 64 == 0 && a.ldm % 64 == 0 && a.ldv % 64 == 0;

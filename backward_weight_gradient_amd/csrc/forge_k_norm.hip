@@ -192,8 +192,8 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_long(const NormArgs a) {
 // ------------------------------------------------------------------------
 constexpr int NB_T = 1024;                // threads of the backward kernel
 // Workgroups of the backward kernels, each with a part of dgamma's sums: one per CU
-// (8192 x 4096 bf16: 36.0 us; 128: 41.2, 512: 38.9, 1024: 45.6; 1021 x 5001: 15.4, 17.9,
-// 18.5, 26.2).
+// (calls in a captured graph, dgamma's second kernel in them, no residual gradient: 8192 x
+// 4096 bf16 36.0 us; 128: 41.2, 512: 38.9, 1024: 45.6; 1021 x 5001 bf16 15.4, 17.9, 18.5, 26.2).
 constexpr int NB_PARTS = 256;
 
 // dx of 8 columns: s (g - n mean) + dr.
@@ -390,8 +390,9 @@ __global__ void __launch_bounds__(NT) k_norm_dgamma(const NormBwdArgs a) {
 // 12.2, 12.8): more lanes than a row needs idle
 // (65536 x 128 forward 12.4 us with 16, 21.6 with 64; 16384 x 1024 21.6 with 64, 27.5
 // with 256, 66 with 1024).  Others are read twice (2048 x 16384: 44 us in registers, 63
-// read twice; backward 43 and 95).  8192 x 4096 bf16 with a residual: 41 us forward
-// (268 MB, 6.5 TB/s), 36 us backward (201 MB, 5.6 TB/s).
+// read twice; backward 43 and 95).  8192 x 4096 bf16 in a captured graph: forward with a
+// residual 42 us (268 MB, 6.4 TB/s), without 22; backward with dgamma 36.5 us (201 MB,
+// 5.5 TB/s), with the residual's gradient as well 46 (268 MB, 5.8 TB/s).
 // ------------------------------------------------------------------------
 constexpr int64_t NORM_REG_COLS = 16384;
 #define FORGE_NORM_SHAPES(X) X(16, 1) X(64, 1) X(64, 2) X(256, 1) X(256, 2) X(1024, 1) X(1024, 2)

@@ -718,8 +718,8 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8_tiny(const KArgs8 a) {
 }
 
 // Which kernel takes a layer (measured with AdamW, fp32 moments):
-//  - the ring of 128 x 128 tiles (k_fused_act8_dma) needs aligned rows in whole 16-byte
-//    segments, and enough tiles: with 128 of them (1024 x 2048) it takes 16.0 / 26.8 /
+//  - the ring of 128 x 128 tiles (k_fused_act8_dma) needs dY's aligned rows in whole 16-byte
+//    segments, K in whole 16-column segments of codes, and enough tiles: with 128 of them (1024 x 2048) it takes 16.0 / 26.8 /
 //    59.9 us at BT 256 / 1024 / 4096, the split kernel 12.4 / 17.9 / 34.9; with 256
 //    (2048 x 2048) 21.1 / 31.7 / 65.4 against 23.3 / 32.7 / 65.9; below BT 128 the
 //    split kernel's joining costs more than it saves (64 x 64: 8.5 against 5.8 us);
@@ -730,8 +730,8 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8_tiny(const KArgs8 a) {
 //    to itself (1024 x 1024: 13.7 against 17.2 us at BT 1024, 46 against 57 at 8192; 336 x
 //    128 33 against 45 at BT 6427), 64 rows and 8 waves beyond (1001 x 1503, 384 tiles of
 //    32 rows: 20.2 against 16.1 us at BT 512, 100 against 72 at 8192);
-//  - everything else of at least 8 x 16 is the split kernel's (3000 x 3000, whose rows
-//    the ring does not take: 290 us at BT 8192, 527 through registers).
+//  - everything else of at least 8 x 16 is the split kernel's (3000 x 3000, where K is no
+//    multiple of 16: 300 us at BT 8192, 527 through registers).
 inline bool act8_ring(const KArgs8& a) { return a.x_dma && a.vec_state && a.K % 4 == 0; }
 inline bool act8_split(const KArgs8& a, bool ring) {
   return a.N >= 8 && a.K >= 16 && (!ring || ((int64_t)a.tiles_n * a.tiles_k < 256 && a.BT >= 128));
