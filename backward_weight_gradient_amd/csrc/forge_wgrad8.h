@@ -719,10 +719,11 @@ __global__ void __launch_bounds__(NT, 2) k_fused_act8_tiny(const KArgs8 a) {
 
 // Which kernel takes a layer (measured with AdamW, fp32 moments):
 //  - the ring of 128 x 128 tiles (k_fused_act8_dma) needs dY's aligned rows in whole 16-byte
-//    segments, K in whole 16-column segments of codes, and enough tiles: with 128 of them (1024 x 2048) it takes 16.0 / 26.8 /
-//    59.9 us at BT 256 / 1024 / 4096, the split kernel 12.4 / 17.9 / 34.9; with 256
-//    (2048 x 2048) 21.1 / 31.7 / 65.4 against 23.3 / 32.7 / 65.9; below BT 128 the
-//    split kernel's joining costs more than it saves (64 x 64: 8.5 against 5.8 us);
+//    segments, K in whole 16-column segments of codes, and enough tiles: with 128 of them
+//    (1024 x 2048) it takes 16.0 / 26.8 / 59.9 us at BT 256 / 1024 / 4096, the split kernel
+//    12.4 / 17.9 / 34.9; with 256 (2048 x 2048) 21.1 / 31.7 / 65.4 against 23.3 / 32.7 /
+//    65.9; below BT 128 the split kernel's joining costs more than it saves (64 x 64: 8.5
+//    against 5.8 us);
 //  - the 256 x 256 tiles (k_fused_act8_wide) pay for long token axes once they fill the
 //    chip: at BT 8192 239 against 302 us for 256 of them (4096 x 4096), but 212
 //    against 109 for 64 (2048 x 2048);
